@@ -106,7 +106,8 @@ enum {
   PA_DEVERR_Q_BOUND = 16,     /* q_len > max_query_len_bound (sequence skipped) */
   PA_DEVERR_ROTARY_POS = 32,  /* position >= max_rotary_positions (row left unrotated) */
   PA_DEVERR_TIMEOUT = 64,     /* an internal wait exceeded its limit (kernel gave up; see pa_last_wait_site) */
-  PA_DEVERR_SLOT = 128        /* slot_mapping entry outside [-1, NB*bs) (row not written) */
+  PA_DEVERR_SLOT = 128,       /* slot_mapping entry outside [-1, NB*bs) (row not written) */
+  PA_DEVERR_ACCEPTED = 256    /* pa_tree_commit: accepted path not ascending or out of range (sequence skipped) */
 };
 
 /* Cache element types (section 8.2, T_CACHE).  8-bit codes are signed and
@@ -309,7 +310,8 @@ enum {
   PA_SITE_PREFILL = 3 << 8,        /* one-tile prefill (head_size 256) */
   PA_SITE_PREFILL_PAIR = 4 << 8,   /* two-tile prefill (head_size 64, 128) */
   PA_SITE_LATENT = 5 << 8,         /* latent decode, mma.sync */
-  PA_SITE_LATENT_TC = 6 << 8       /* latent decode, tcgen05 */
+  PA_SITE_LATENT_TC = 6 << 8,      /* latent decode, tcgen05 */
+  PA_SITE_TREE = 7 << 8            /* tree attention */
 };
 /* The wait-site id read (and cleared) by the last pa_check_device_error on
  * h; 0 when no wait gave up. */
@@ -413,6 +415,169 @@ PA_API int pa_last_launch_count(pa_handle h);
  * SM; without it they are the launched grids). */
 enum { PA_STEP_COUNTS = 6 };
 PA_API pa_status pa_last_step_counts(pa_handle h, int32_t* counts);
+
+/* ---- speculative decoding: trees of drafted tokens ----
+ *
+ * The new tokens of a sequence may be a tree of drafted tokens instead of a
+ * run.  Draft token j of sequence b (packed row t = cum[b] + j, parents
+ * before children) occupies cache slot past[b] + j until the step is decided,
+ * but stands at its own position (past[b] + its depth, as a rule) and attends
+ * to the cached context and to its own ancestors.  The calls, in order:
+ *   pa_tree_write      Q and K rotated at explicit positions, Q to a dense
+ *                      copy, K and V to slots past[b] + j of the paged pool
+ *   pa_tree_attention  attention under a mask over the draft tokens
+ *   pa_tree_commit     the accepted path's rows moved to the front of the
+ *                      draft slots, in every layer's pools
+ * pa_rotary is the same rotation on plain rows, and its gradient.
+ *
+ * Padding: rows at and behind cum[batch] (cum[batch] <= token_count) are
+ * neither read nor written, so a captured step may be sized for more tokens
+ * than it holds. */
+
+/* Element types of pa_rotary. */
+enum { PA_ROTARY_FP16 = 0, PA_ROTARY_BF16 = 1, PA_ROTARY_FP32 = 2 };
+
+/* Frequency scalings for contexts longer than the trained one (R =
+ * rotary_dim, f_i = base^(-2i/R) radians per position for pair i, s =
+ * factor, L = original_positions):
+ *   NONE           f_i
+ *   LINEAR         f_i / s
+ *   BASE           (base * s^(R/(R-2)))^(-2i/R)
+ *   BY_PARTS       f_i/s * r_i + f_i * (1 - r_i), r_i = clamp((i - lo)/(hi - lo), 0, 1),
+ *                  lo = max(floor(at(high)), 0), hi = min(ceil(at(low)), R - 1),
+ *                  at(turns) = R ln(L/(2 pi turns)) / (2 ln base);
+ *                  attention factor 0.1 ln(s) + 1
+ *   BY_WAVELENGTH  f_i/s * (1 - k_i) + f_i * k_i, k_i = clamp((L f_i/(2 pi) - low)/(high - low), 0, 1)
+ * low < high are turns over the L original positions. */
+enum {
+  PA_ROTARY_SCALE_NONE = 0,
+  PA_ROTARY_SCALE_LINEAR = 1,
+  PA_ROTARY_SCALE_BASE = 2,
+  PA_ROTARY_SCALE_BY_PARTS = 3,
+  PA_ROTARY_SCALE_BY_WAVELENGTH = 4
+};
+typedef struct {
+  int type;                  /* PA_ROTARY_SCALE_* */
+  double base;               /* > 1 */
+  double factor;             /* s >= 1; read unless NONE */
+  double original_positions; /* L > 0; BY_PARTS and BY_WAVELENGTH */
+  double low, high;          /* 0 < low < high; BY_PARTS and BY_WAVELENGTH */
+} pa_rotary_scaling;
+
+/* Host only: steps[i] = the frequency of pair i as 2^-64 turns per position,
+ * round(f_i / (2 pi) * 2^64) mod 2^64, i < rotary_dim / 2.  The phase of
+ * position p is then (p * steps[i]) mod 2^64, exact in wrapping 64-bit
+ * arithmetic however far p is (also negative).  *attention_factor (may be
+ * NULL) receives the factor on cos and sin (1 except BY_PARTS).  The caller
+ * copies the steps to the device; own frequencies may be given the same way. */
+PA_API pa_status pa_rotary_steps(const pa_rotary_scaling* scaling, int rotary_dim, uint64_t* steps,
+                                 float* attention_factor);
+
+/* Row geometry of a rotation. */
+typedef struct {
+  int head_size;          /* D, multiple of 8, at most 512 */
+  int rotary_dim;         /* R, multiple of 16; 0 => D */
+  int rotary_offset;      /* first rotated channel, multiple of 8 */
+  int interleaved;        /* 0: pairs (i, i+R/2); 1: pairs (2i, 2i+1) */
+  int dtype;              /* PA_ROTARY_* */
+  float attention_factor; /* m, finite; 1 by default */
+  int conjugate;          /* 1: rotate by -angle; with the same m this is the gradient of the rotation
+                             (dx from dy), with 1/m it is its inverse */
+} pa_rotary_config;
+/* Zeroes *rc, attention_factor 1. */
+PA_API void pa_rotary_config_init(pa_rotary_config* rc);
+
+/* Rotates token_count rows of Q and K at positions[t] (int32, device, any
+ * value): per pair, with a = 2 pi frac(positions[t] * steps[i] / 2^64),
+ *   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a)
+ * in fp32, rounded once to the type; the other channels are copied.
+ * Row t of a tensor starts at t * stride elements (a multiple of 8, at least
+ * heads * D; 0 => heads * D), so slices of packed rows are taken and written
+ * in place.  query_out == query with equal strides rotates in place; an
+ * output that overlaps its input in any other way is refused, and so are
+ * outputs that overlap each other or the other input.  Overlap is decided by
+ * whole ranges of rows, save that two slices of one row layout (equal
+ * strides, disjoint columns) do not overlap.  num_heads or kv_num_heads 0
+ * leaves that tensor out.  Runs on the current device; keeps nothing, so calls may overlap. */
+PA_API pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int32_t* positions,
+                           int token_count, int num_heads, const void* query, int64_t query_stride,
+                           void* query_out, int64_t query_out_stride, int kv_num_heads, const void* key,
+                           int64_t key_stride, void* key_out, int64_t key_out_stride, void* stream);
+
+typedef struct pa_tree_handle_s* pa_tree_handle;
+
+/* A layer's handle for trees of at most max_draft_tokens (1..256) drafted
+ * tokens per sequence.  cfg is the layer's pa_config; read are the heads,
+ * head_size, paging, scale, softcap, local_window_size, max_batch,
+ * max_tokens, max_kv_len_bound and cache_dtype (PA_CACHE_FP16 or
+ * PA_CACHE_BF16, the activations' type too).  Its rotary fields are not read
+ * here (positions are explicit; pa_tree_write takes a pa_rotary_config).
+ * PA_NOT_SUPPORTED: head_size other than 64 and 128, 8-bit caches, the latent
+ * layout, packed_qkv, qk_norm.  Allocates the workspace (split-KV partials,
+ * error word) on the current device.
+ * One handle's pa_tree_attention calls share that workspace: calls (and
+ * replays of graphs captured from them) on one handle must not overlap on the
+ * GPU; use a handle per stream.  pa_tree_write and pa_tree_commit do not use it. */
+PA_API pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_handle* out);
+PA_API pa_status pa_tree_destroy(pa_tree_handle h);
+
+/* pa_rotary on Q and K (rc->head_size and dtype must be the handle's), then
+ * K and V to slots past[b] + j of the paged pools through block_table (a -1
+ * entry writes nothing).  query_out [T, H*D] dense; query_out may be query
+ * when query_stride is H*D.  V rows are copied bit for bit.  positions [T]. */
+PA_API pa_status pa_tree_write(pa_tree_handle h, const pa_rotary_config* rc, const uint64_t* steps,
+                               const int32_t* positions, const void* query, int64_t query_stride,
+                               const void* key, int64_t key_stride, const void* value, int64_t value_stride,
+                               void* query_out, void* key_cache, void* value_cache, const int32_t* block_table,
+                               const int32_t* cumulative_sequence_lengths, const int32_t* past_sequence_lengths,
+                               int batch, int token_count, void* stream);
+
+/* Optional inputs of pa_tree_attention; any pointer may be NULL. */
+typedef struct {
+  const int32_t* positions;     /* [T]; NULL => past[b] + j.  Used by the window and the distance bias */
+  const uint32_t* tree_mask;    /* [T, ceil(max_draft_tokens/32)]: bit i%32 of word i/32 of row t admits draft
+                                   token i of the same sequence; bits at and above its length are ignored, no bit
+                                   is implied.  NULL => causal (i <= j) */
+  const float* distance_slopes; /* [H]: adds slope_h * (kpos - qpos) to the scores, after softcap */
+  const void* head_sink;        /* [H], the cache's type: one extra logit in the denominator */
+} pa_tree_inputs;
+
+/* Attention of every packed query row over its sequence's cache (the draft
+ * rows already written).  Row (t, h) admits every context slot p < past[b]
+ * (at position p; -1 pages are masked) and draft token i under the mask (at
+ * positions[cum[b] + i]); with local_window_size W only keys at positions
+ * > max(positions[t], past[b]) - W.  x = scale <q, k>, softcapped, plus the
+ * bias; output = sum softmax(x) v, 0 when nothing is admitted.  A key that a
+ * row does not admit never reaches that row, whatever its K and V hold
+ * (window edges: V must be finite there).  query, output [T, H*D]; output
+ * must not overlap the inputs.  P is rounded to the 16-bit type for the P*V
+ * contraction; scores, sums and the output accumulate in fp32. */
+PA_API pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key_cache,
+                                   const void* value_cache, const int32_t* block_table,
+                                   const int32_t* cumulative_sequence_lengths,
+                                   const int32_t* past_sequence_lengths, int batch, int token_count,
+                                   const pa_tree_inputs* inputs, void* output, void* stream);
+
+/* For every sequence b and layer l: slot past[b] + i receives the K and V rows
+ * of slot past[b] + accepted[b * max_accepted + i], i < accepted_count[b].
+ * accepted rows are strictly ascending draft indexes (a path in packed
+ * order) with max_accepted <= max_draft_tokens.  key_caches and value_caches
+ * are HOST arrays of num_layers device pointers to pools of the handle's
+ * geometry, none overlapping another.  new_past [batch] (may be NULL, must
+ * not overlap past) receives past[b] + accepted_count[b].  A sequence with a
+ * bad path or length is left as it was (new_past = past) and flagged; a -1
+ * page moves nothing. */
+PA_API pa_status pa_tree_commit(pa_tree_handle h, void* const* key_caches, void* const* value_caches,
+                                int num_layers, const int32_t* block_table,
+                                const int32_t* past_sequence_lengths, const int32_t* accepted,
+                                const int32_t* accepted_count, int max_accepted, int batch, int32_t* new_past,
+                                void* stream);
+
+/* Synchronises the handle's device, reads and clears the handle's error word
+ * (PA_DEVERR_*).  Not capturable. */
+PA_API pa_status pa_tree_check_device_error(pa_tree_handle h, int* code);
+/* Message of the last failure on h (NULL: on this thread). */
+PA_API const char* pa_tree_last_error_message(pa_tree_handle h);
 
 #ifdef __cplusplus
 }

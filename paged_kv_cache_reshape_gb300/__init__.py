@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_INVALID_ARGUMENT", 2: "PA_NOT_SUPPORTED", 3: 
 PA_DEVERR_CUM, PA_DEVERR_BLOCK_ID, PA_DEVERR_PAST = 1, 2, 4
 PA_DEVERR_KV_BOUND, PA_DEVERR_Q_BOUND, PA_DEVERR_ROTARY_POS, PA_DEVERR_TIMEOUT = 8, 16, 32, 64
 PA_DEVERR_SLOT = 128
+PA_DEVERR_ACCEPTED = 256
 
 PA_OPT_SPLIT_KEYS, PA_OPT_NO_WINDOW_PRUNE, PA_OPT_KERNEL_TIMING, PA_OPT_DECODE_MAX_ROWS = 1, 2, 3, 4
 PA_OPT_DECODE_ITEMS_PER_CTA = 5
@@ -30,6 +31,7 @@ PA_OPT_LATENT_TCGEN05 = 6
 PA_OPT_PREFILL_SMS, PA_OPT_WAIT_PROBE = 7, 8
 PA_SITE_DECODE, PA_SITE_COMBINE, PA_SITE_PREFILL, PA_SITE_PREFILL_PAIR, PA_SITE_LATENT, PA_SITE_LATENT_TC = (
     k << 8 for k in range(1, 7))
+PA_SITE_TREE = 7 << 8
 PA_STEP_COUNTS = 6
 STEP_COUNT_NAMES = ("n_dec", "n_pre", "n_comb", "split_keys", "pre_ctas", "dec_ctas")
 PA_STAGE_WORKLIST, PA_STAGE_CACHE_WRITE, PA_STAGE_DECODE, PA_STAGE_PREFILL, PA_STAGE_COMBINE = range(5)
@@ -38,11 +40,17 @@ PA_CACHE_FP16, PA_CACHE_INT8, PA_CACHE_FP8_E4M3, PA_CACHE_BF16 = 0, 1, 2, 3
 PA_ACT_DEFAULT, PA_ACT_BF16 = 0, 1
 PA_QUANT_NONE, PA_QUANT_PER_TENSOR, PA_QUANT_PER_CHANNEL = 0, 1, 2
 PA_LAYOUT_SEPARATE, PA_LAYOUT_LATENT = 0, 1
+PA_ROTARY_FP16, PA_ROTARY_BF16, PA_ROTARY_FP32 = 0, 1, 2
+(PA_ROTARY_SCALE_NONE, PA_ROTARY_SCALE_LINEAR, PA_ROTARY_SCALE_BASE, PA_ROTARY_SCALE_BY_PARTS,
+ PA_ROTARY_SCALE_BY_WAVELENGTH) = range(5)
 
 EXPORTED = ("pa_config_init", "pa_validate_config", "pa_check_step", "pa_create", "pa_cache_write",
             "pa_forward", "pa_check_device_error", "pa_last_error_message", "pa_destroy",
             "pa_set_option", "pa_kernel_time_ms", "pa_last_launch_count", "pa_forward_no_alloc",
-            "pa_cache_write_ex", "pa_forward_ex", "pa_last_wait_site", "pa_last_step_counts")
+            "pa_cache_write_ex", "pa_forward_ex", "pa_last_wait_site", "pa_last_step_counts",
+            "pa_rotary_config_init", "pa_rotary_steps", "pa_rotary", "pa_tree_create", "pa_tree_destroy",
+            "pa_tree_write", "pa_tree_attention", "pa_tree_commit", "pa_tree_check_device_error",
+            "pa_tree_last_error_message")
 
 
 class pa_config(ctypes.Structure):
@@ -61,6 +69,20 @@ class pa_extra_inputs(ctypes.Structure):
     _fields_ = [("head_sink", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("slot_mapping", ctypes.c_void_p), ("q_norm_weight", ctypes.c_void_p),
                 ("k_norm_weight", ctypes.c_void_p)]
+
+
+class pa_rotary_scaling(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int)] + [(n, ctypes.c_double) for n in ("base", "factor", "original_positions",
+                                                                         "low", "high")]
+
+
+class pa_rotary_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("head_size", "rotary_dim", "rotary_offset", "interleaved", "dtype")] + [
+        ("attention_factor", ctypes.c_float), ("conjugate", ctypes.c_int)]
+
+
+class pa_tree_inputs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("positions", "tree_mask", "distance_slopes", "head_sink")]
 
 
 class PAError(RuntimeError):
@@ -103,8 +125,23 @@ def lib():
         L.pa_last_launch_count.restype = I
         L.pa_last_wait_site.argtypes = [P]
         L.pa_last_step_counts.argtypes = [P, ctypes.POINTER(I)]
+        L64, RC = ctypes.c_int64, ctypes.POINTER(pa_rotary_config)
+        L.pa_rotary_config_init.argtypes = [RC]
+        L.pa_rotary_config_init.restype = None
+        L.pa_rotary_steps.argtypes = [ctypes.POINTER(pa_rotary_scaling), I, ctypes.POINTER(ctypes.c_uint64),
+                                      ctypes.POINTER(ctypes.c_float)]
+        L.pa_rotary.argtypes = [RC, P, P, I, I, P, L64, P, L64, I, P, L64, P, L64, P]
+        L.pa_tree_create.argtypes = [CFG, I, ctypes.POINTER(P)]
+        L.pa_tree_destroy.argtypes = [P]
+        L.pa_tree_write.argtypes = [P, RC, P, P, P, L64, P, L64, P, L64, P, P, P, P, P, P, I, I, P]
+        L.pa_tree_attention.argtypes = [P, P, P, P, P, P, P, I, I, ctypes.POINTER(pa_tree_inputs), P, P]
+        L.pa_tree_commit.argtypes = [P, P, P, I, P, P, P, P, I, I, P, P]
+        L.pa_tree_check_device_error.argtypes = [P, ctypes.POINTER(I)]
+        L.pa_tree_last_error_message.argtypes = [P]
+        L.pa_tree_last_error_message.restype = ctypes.c_char_p
         for n in EXPORTED:
-            if n not in ("pa_config_init", "pa_last_error_message", "pa_last_launch_count"):
+            if n not in ("pa_config_init", "pa_last_error_message", "pa_last_launch_count", "pa_rotary_config_init",
+                         "pa_tree_last_error_message"):
                 getattr(L, n).restype = I
         _lib = L
     return _lib
@@ -356,6 +393,156 @@ class PagedAttention:
     def close(self):
         if self.handle is not None:
             pa_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---- speculative decoding: trees of drafted tokens (include/pa.h)
+
+
+def make_rotary_config(head_size, rotary_dim=0, rotary_offset=0, interleaved=0, dtype=PA_ROTARY_FP16,
+                       attention_factor=1.0, conjugate=0) -> pa_rotary_config:
+    rc = pa_rotary_config()
+    lib().pa_rotary_config_init(ctypes.byref(rc))
+    rc.head_size, rc.rotary_dim, rc.rotary_offset, rc.interleaved = head_size, rotary_dim, rotary_offset, interleaved
+    rc.dtype, rc.attention_factor, rc.conjugate = dtype, attention_factor, conjugate
+    return rc
+
+
+def pa_rotary_steps(rotary_dim, type=PA_ROTARY_SCALE_NONE, base=10000.0, factor=1.0, original_positions=0.0,
+                    low=1.0, high=4.0):
+    """(steps, attention_factor): the phase steps as a list of rotary_dim / 2
+    whole numbers in [0, 2^64).  As a tensor they are int64 (the same bits):
+    rotary_steps_tensor()."""
+    sc = pa_rotary_scaling(type, base, factor, original_positions, low, high)
+    steps, m = (ctypes.c_uint64 * max(rotary_dim // 2, 1))(), ctypes.c_float(0.0)
+    _check(lib().pa_rotary_steps(ctypes.byref(sc), rotary_dim, steps, ctypes.byref(m)))
+    return list(steps)[:rotary_dim // 2], m.value
+
+
+def rotary_steps_tensor(steps, device="cuda"):
+    """Phase steps as the int64 device tensor that pa_rotary and pa_tree_write take."""
+    import torch
+    return torch.tensor([v - (1 << 64) if v >> 63 else v for v in steps], dtype=torch.int64, device=device)
+
+
+def _row_stride(t):
+    if t.stride(-1) != 1 or t.dim() != 2:
+        raise PAError(PA_INVALID_ARGUMENT, "rows must be 2-D with contiguous columns")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def pa_rotary(rc, steps, positions, token_count, num_heads, query, query_out, kv_num_heads=0, key=None,
+              key_out=None, stream=None):
+    """Rotates the rows of query [T, num_heads * D] and key; row strides are the tensors' own."""
+    st = lib().pa_rotary(rc, steps.data_ptr(), positions.data_ptr(), token_count, num_heads,
+                         query.data_ptr() if num_heads else None, _row_stride(query) if num_heads else 0,
+                         query_out.data_ptr() if num_heads else None, _row_stride(query_out) if num_heads else 0,
+                         kv_num_heads, key.data_ptr() if kv_num_heads else None,
+                         _row_stride(key) if kv_num_heads else 0, key_out.data_ptr() if kv_num_heads else None,
+                         _row_stride(key_out) if kv_num_heads else 0, stream)
+    if st:
+        _check(st)
+
+
+def _tree_check(status, h):
+    if status != PA_OK:
+        raise PAError(status, lib().pa_tree_last_error_message(h).decode())
+
+
+def pa_tree_create(cfg: pa_config, max_draft_tokens):
+    h = ctypes.c_void_p()
+    _tree_check(lib().pa_tree_create(ctypes.byref(cfg), max_draft_tokens, ctypes.byref(h)), None)
+    return h
+
+
+def pa_tree_destroy(h):
+    _tree_check(lib().pa_tree_destroy(h), None)
+
+
+def pa_tree_write(h, rc, steps, positions, query, key, value, query_out, key_cache, value_cache, block_table,
+                  cumulative_sequence_lengths, past_sequence_lengths, batch, token_count, stream=None):
+    st = lib().pa_tree_write(h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query),
+                             key.data_ptr(), _row_stride(key), value.data_ptr(), _row_stride(value),
+                             query_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                             block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
+                             past_sequence_lengths.data_ptr(), batch, token_count, stream)
+    if st:
+        _tree_check(st, h)
+
+
+def pa_tree_attention(h, query, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+                      past_sequence_lengths, batch, token_count, output, positions=None, tree_mask=None,
+                      distance_slopes=None, head_sink=None, stream=None):
+    x = pa_tree_inputs(None if positions is None else positions.data_ptr(),
+                       None if tree_mask is None else tree_mask.data_ptr(),
+                       None if distance_slopes is None else distance_slopes.data_ptr(),
+                       None if head_sink is None else head_sink.data_ptr())
+    st = lib().pa_tree_attention(h, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                 block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
+                                 past_sequence_lengths.data_ptr(), batch, token_count, x, output.data_ptr(), stream)
+    if st:
+        _tree_check(st, h)
+
+
+class layer_pools:
+    """The pools of a model's layers as pa_tree_commit takes them (holds the tensors)."""
+
+    def __init__(self, key_caches, value_caches):
+        self.tensors = (list(key_caches), list(value_caches))
+        if len(self.tensors[0]) != len(self.tensors[1]):
+            raise PAError(PA_INVALID_ARGUMENT, "key_caches and value_caches must have one pool per layer each")
+        self.num_layers = len(self.tensors[0])
+        self.keys, self.values = ((ctypes.c_void_p * self.num_layers)(*[t.data_ptr() for t in ts])
+                                  for ts in self.tensors)
+
+
+def pa_tree_commit(h, layers, block_table, past_sequence_lengths, accepted, accepted_count, batch, new_past=None,
+                   stream=None):
+    """accepted [batch, max_accepted] int32 (contiguous), accepted_count [batch]; layers: a layer_pools."""
+    st = lib().pa_tree_commit(h, layers.keys, layers.values, layers.num_layers, block_table.data_ptr(),
+                              past_sequence_lengths.data_ptr(), accepted.data_ptr(), accepted_count.data_ptr(),
+                              accepted.shape[1], batch, None if new_past is None else new_past.data_ptr(), stream)
+    if st:
+        _tree_check(st, h)
+
+
+def pa_tree_check_device_error(h) -> int:
+    code = ctypes.c_int(0)
+    st = lib().pa_tree_check_device_error(h, ctypes.byref(code))
+    if st not in (PA_OK, PA_DEVICE_DATA_ERROR):
+        _tree_check(st, h)
+    return code.value
+
+
+class PagedTree:
+    """A handle for trees of drafted tokens over one layer configuration (owns the device workspace)."""
+
+    def __init__(self, cfg: pa_config, max_draft_tokens: int):
+        self.handle = None
+        self.cfg, self.max_draft_tokens = cfg, max_draft_tokens
+        self.handle = pa_tree_create(cfg, max_draft_tokens)
+
+    def write(self, *args, **kw):
+        pa_tree_write(self.handle, *args, **kw)
+
+    def attention(self, *args, **kw):
+        pa_tree_attention(self.handle, *args, **kw)
+
+    def commit(self, *args, **kw):
+        pa_tree_commit(self.handle, *args, **kw)
+
+    def device_error(self) -> int:
+        return pa_tree_check_device_error(self.handle)
+
+    def close(self):
+        if self.handle is not None:
+            pa_tree_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -1460,3 +1460,23 @@ extern "C" pa_status pa_forward_no_alloc(const pa_config* cfg, const void* query
   if (e != cudaSuccess) return cuda_fail(nullptr, e, "combine launch");
   return PA_OK;
 }
+
+// ---- helpers shared with the tree operators (tree.h)
+namespace pa {
+
+pa_status host_fail(pa_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_msg = buf;
+  return st;
+}
+
+bool encode_rows_map(CUtensorMap* m, const void* base, int D, int heads_total, long long rows_total, int heads_box,
+                     int rows_box) {
+  return encode_map(m, base, D, heads_total, rows_total, heads_box, rows_box);
+}
+
+}  // namespace pa

@@ -1,0 +1,89 @@
+// Internal structures of the tree operators (rotary at explicit positions,
+// attention for trees of drafted tokens, commit of the accepted path).
+#pragma once
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/pa.h"
+
+namespace pa {
+
+// ---- shared host helpers (api.cu)
+// Records the thread's last message (pa_last_error_message(NULL)) and returns st.
+pa_status host_fail(pa_status st, const char* fmt, ...);
+// 3-D view {D, heads_total, rows_total} of rows of heads, box {64, heads_box, rows_box}, 128-byte swizzle.
+bool encode_rows_map(CUtensorMap* m, const void* base, int D, int heads_total, long long rows_total, int heads_box,
+                     int rows_box);
+
+// ---- rotary (rotary.cu)
+struct RotaryRows {  // rows of one tensor; nheads == 0: absent
+  const void* src;
+  void* dst;           // NULL for rows that go to the pool
+  long long src_stride, dst_stride;  // elements
+  int nheads;
+};
+
+struct RotaryParams {
+  RotaryRows q, k, v;  // v: copied rows (pool mode only)
+  const unsigned long long* steps;
+  const int* positions;
+  int T;
+  int D, R, off;
+  float factor, sin_sign;
+  int parts;           // warps per token, each a contiguous share of the token's head items
+  // pool mode (key_cache != NULL): K and V rows to slots of the paged pool
+  void* key_cache;
+  void* value_cache;
+  const int* block_table;
+  const int* cum;
+  const int* past;
+  int batch, bs, NB, MB;
+  int* err;
+};
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, int interleaved, cudaStream_t s);
+
+// ---- commit (tree_commit.cu)
+constexpr int kCommitLayers = 128;  // layers of one launch
+struct CommitParams {
+  void* pools[2 * kCommitLayers];   // K, V, K, V, ...
+  int n_pools;
+  int row_vecs;                     // 16-byte vectors of one slot's row
+  const int* block_table;
+  const int* past;
+  const int* accepted;
+  const int* count;
+  int max_accepted, batch, bs, NB, MB;
+  int* new_past;
+  int* err;
+};
+cudaError_t launch_commit(const CommitParams& p, int num_sms, cudaStream_t s);
+
+// ---- tree attention (tree_attention.cu)
+constexpr int kTreeMaxDraft = 256;
+constexpr int kTreeMaxWords = kTreeMaxDraft / 32;
+
+struct TreeParams {
+  const __half* query;
+  const __half* key_cache;
+  const __half* value_cache;
+  const int* block_table;
+  const int* cum;
+  const int* past;
+  const int* positions;      // NULL: past + j
+  const uint32_t* mask;      // NULL: causal
+  const float* slopes;       // NULL: none
+  const __half* head_sink;   // NULL: none
+  __half* out;
+  int batch, T;
+  int H, Hk, G, D;
+  int bs, NB, MB, log_bs;
+  int max_draft, words, max_kv;
+  int window;
+  float scale, softcap;
+  int* err;
+};
+cudaError_t launch_tree_simple(const TreeParams& p, int bf16, cudaStream_t s);
+
+}  // namespace pa
