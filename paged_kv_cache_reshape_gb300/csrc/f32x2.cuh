@@ -1,0 +1,52 @@
+// Softmax helpers of the two-tile tcgen05 kernels: maxima by three-input max
+// and two fp32 lanes per instruction.
+#pragma once
+#include <stdint.h>
+
+namespace pa {
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Maximum of N values as a tree of three-input max.
+template <int N>
+__device__ __forceinline__ float max_tree(const float* v) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    constexpr int M = (N + 2) / 3;
+    float w[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      if (3 * k + 2 < N) w[k] = max3(v[3 * k], v[3 * k + 1], v[3 * k + 2]);
+      else if (3 * k + 1 < N) w[k] = fmaxf(v[3 * k], v[3 * k + 1]);
+      else w[k] = v[3 * k];
+    }
+    return max_tree<M>(w);
+  }
+}
+
+// Two fp32 lanes in one 64-bit register (Blackwell f32x2 arithmetic).
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+}  // namespace pa

@@ -134,7 +134,8 @@ enum WaitKernel {
   kSitePrefill = 3 << 8,
   kSitePrefillPair = 4 << 8,
   kSiteMla = 5 << 8,
-  kSiteMlaTc = 6 << 8
+  kSiteMlaTc = 6 << 8,
+  kSiteTree = 7 << 8
 };
 
 // Records a wait that gave up: the error bit, and the site id if it is the

@@ -64,9 +64,16 @@ cudaError_t launch_commit(const CommitParams& p, int num_sms, cudaStream_t s);
 constexpr int kTreeMaxDraft = 256;
 constexpr int kTreeMaxWords = kTreeMaxDraft / 32;
 
+// A unit of work whose partial results lie in several CTAs' slots.
+struct Cut {
+  int rows;    // rows of the unit's partial results; 0: none starts in this CTA's range
+  int slot0;   // slot of the first partial; the next ones are slots 2 (c + 1), 2 (c + 2), ...
+  int more;    // CTAs behind this one that hold a partial
+  int t0, ntok, k;
+  int pad[2];
+};
+
 struct TreeParams {
-  const __half* query;
-  const __half* key_cache;
   const __half* value_cache;
   const int* block_table;
   const int* cum;
@@ -78,12 +85,21 @@ struct TreeParams {
   __half* out;
   int batch, T;
   int H, Hk, G, D;
-  int bs, NB, MB, log_bs;
+  int tile_tokens;           // tokens of a 128-row tile
+  int bs, NB, MB, log_bs, log_page_rows, oob_row;
   int max_draft, words, max_kv;
-  int window;
+  int window, min_tiles;
   float scale, softcap;
+  // workspace
+  Cut* cuts;                 // [CTAs]
+  float2* part_ml;           // [2 CTAs][part_rows]
+  float4* part_o;            // [2 CTAs][D / 4][part_rows]
+  int part_rows;
   int* err;
+  int* err_site;
 };
-cudaError_t launch_tree_simple(const TreeParams& p, int bf16, cudaStream_t s);
+cudaError_t tree_configure(int head_size, int bf16);
+cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                        int bf16, int grid, cudaStream_t s);
 
 }  // namespace pa

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/pa.h"
+#include "step.h"
 #include "tree.h"
 
 struct pa_tree_handle_s {
@@ -19,8 +20,12 @@ struct pa_tree_handle_s {
   int max_draft = 0, words = 0, max_kv = 0;
   float scale = 0.f;
   bool bf16 = false;
+  int tile_tokens = 1, part_rows = 0;
   void* ws = nullptr;
   int* err = nullptr;
+  pa::Cut* cuts = nullptr;
+  float2* part_ml = nullptr;
+  float4* part_o = nullptr;
   std::string msg = "no error";
 };
 
@@ -272,15 +277,30 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   h->max_kv = c.max_kv_len_bound > 0 ? std::min(c.max_kv_len_bound, kv_cap) : kv_cap;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
-  if (e == cudaSuccess) e = cudaMalloc(&h->ws, 256);
-  if (e == cudaSuccess) e = cudaMemset(h->ws, 0, 256);
+  if (e == cudaSuccess) e = pa::tree_configure(c.head_size, h->bf16);
+  // Workspace: error word, the cut units, and two partial results per CTA
+  // (256-byte aligned pieces).
+  const int G = c.num_heads / c.kv_num_heads;
+  h->tile_tokens = pa::kPrefillRows / G;
+  h->part_rows = max_draft_tokens > h->tile_tokens ? 2 * pa::kPrefillRows : (max_draft_tokens * G + 31) / 32 * 32;
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t slots = 2 * (size_t)h->num_sms, D = c.head_size;
+  const size_t o_cut = 256, o_ml = o_cut + up(sizeof(pa::Cut) * h->num_sms);
+  const size_t o_po = o_ml + up(sizeof(float2) * slots * h->part_rows);
+  const size_t ws_bytes = o_po + sizeof(float) * slots * h->part_rows * D;
+  if (e == cudaSuccess) e = cudaMalloc(&h->ws, ws_bytes);
+  if (e == cudaSuccess) e = cudaMemset(h->ws, 0, o_ml);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     if (h->ws) cudaFree(h->ws);
     delete h;
     return tree_cuda_fail(nullptr, e, "pa_tree_create");
   }
-  h->err = static_cast<int*>(h->ws);
+  uint8_t* w = static_cast<uint8_t*>(h->ws);
+  h->err = reinterpret_cast<int*>(w);
+  h->cuts = reinterpret_cast<pa::Cut*>(w + o_cut);
+  h->part_ml = reinterpret_cast<float2*>(w + o_ml);
+  h->part_o = reinterpret_cast<float4*>(w + o_po);
   *out = h;
   return PA_OK;
 }
@@ -390,8 +410,6 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
     return tree_fail(h, PA_INVALID_ARGUMENT, "output must not overlap query or the pools");
   OnDevice g(h->device);
   pa::TreeParams p{};
-  p.query = static_cast<const __half*>(query);
-  p.key_cache = static_cast<const __half*>(key_cache);
   p.value_cache = static_cast<const __half*>(value_cache);
   p.block_table = block_table;
   p.cum = cum;
@@ -418,8 +436,24 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   p.window = c.local_window_size;
   p.scale = h->scale;
   p.softcap = c.softcap;
+  p.tile_tokens = h->tile_tokens;
+  const int page_rows = std::min(c.block_size, pa::kPrefillKeys);
+  p.log_page_rows = 0;
+  while ((1 << p.log_page_rows) < page_rows) ++p.log_page_rows;
+  p.oob_row = c.num_blocks * c.block_size;
+  p.min_tiles = 1;
+  p.cuts = h->cuts;
+  p.part_ml = h->part_ml;
+  p.part_o = h->part_o;
+  p.part_rows = h->part_rows;
   p.err = h->err;
-  cudaError_t e = pa::launch_tree_simple(p, h->bf16, static_cast<cudaStream_t>(stream));
+  p.err_site = h->err + 1;
+  CUtensorMap tq, tk, tv;
+  if (!pa::encode_rows_map(&tq, query, D, H, token_count, p.G, p.tile_tokens) ||
+      !pa::encode_rows_map(&tk, key_cache, D, Hk, (long long)c.num_blocks * c.block_size, 1, page_rows) ||
+      !pa::encode_rows_map(&tv, value_cache, D, Hk, (long long)c.num_blocks * c.block_size, 1, page_rows))
+    return tree_fail(h, PA_CUDA_ERROR, "cuTensorMapEncodeTiled failed");
+  cudaError_t e = pa::launch_tree(tq, tk, tv, p, h->bf16, h->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return tree_cuda_fail(h, e, "tree attention launch");
   return PA_OK;
 }
