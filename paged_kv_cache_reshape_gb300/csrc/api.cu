@@ -1479,4 +1479,18 @@ bool encode_rows_map(CUtensorMap* m, const void* base, int D, int heads_total, l
   return encode_map(m, base, D, heads_total, rows_total, heads_box, rows_box);
 }
 
+bool encode_groups_map(CUtensorMap* m, const void* base, int D, int Hk, long long rows_total, int rows_box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)Hk * D * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)(D / 64), (cuuint64_t)(rows_total / 8), (cuuint64_t)Hk};
+  cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)D * 2};
+  cuuint32_t box[5] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(rows_box / 8), 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace pa

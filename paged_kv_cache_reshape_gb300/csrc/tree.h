@@ -16,6 +16,9 @@ pa_status host_fail(pa_status st, const char* fmt, ...);
 // 3-D view {D, heads_total, rows_total} of rows of heads, box {64, heads_box, rows_box}, 128-byte swizzle.
 bool encode_rows_map(CUtensorMap* m, const void* base, int D, int heads_total, long long rows_total, int heads_box,
                      int rows_box);
+// 5-D view {64 channels, 8 rows, D/64 chunks, rows_total/8 groups, Hk} of a pool: a box {64, 8, D/64, rows_box/8, 1}
+// is one head's rows laid out [group][chunk][row][128 B] with the 128-byte swizzle.
+bool encode_groups_map(CUtensorMap* m, const void* base, int D, int Hk, long long rows_total, int rows_box);
 
 // ---- rotary (rotary.cu)
 struct RotaryRows {  // rows of one tensor; nheads == 0: absent
@@ -64,13 +67,18 @@ cudaError_t launch_commit(const CommitParams& p, int num_sms, cudaStream_t s);
 constexpr int kTreeMaxDraft = 256;
 constexpr int kTreeMaxWords = kTreeMaxDraft / 32;
 
-// A unit of work whose partial results lie in several CTAs' slots.
+// A unit of work whose partial results lie in several chunks' slots.
 struct Cut {
-  int rows;    // rows of the unit's partial results; 0: none starts in this CTA's range
-  int slot0;   // slot of the first partial; the next ones are slots 2 (c + 1), 2 (c + 2), ...
-  int more;    // CTAs behind this one that hold a partial
+  int rows;          // rows of the unit's partial results
+  int slot0, slot1;  // slots of the first and second partial; later ones are 2 Hk slots further each
+  int more;          // partials behind the first
   int t0, ntok, k;
-  int pad[2];
+  int pad;
+};
+
+struct TreeCounters {  // zero between calls
+  int n_cuts;
+  int joined;   // blocks of the joining kernel that are done
 };
 
 struct TreeParams {
@@ -88,12 +96,17 @@ struct TreeParams {
   int tile_tokens;           // tokens of a 128-row tile
   int bs, NB, MB, log_bs, log_page_rows, oob_row;
   int max_draft, words, max_kv;
-  int window, min_tiles;
+  int window;
+  int n_ranges, min_len;     // ranges of the line; the smallest, in tiles
+  int q_tiles;               // 2 when a unit may have two row tiles
   float scale, softcap;
   // workspace
-  Cut* cuts;                 // [CTAs]
-  float2* part_ml;           // [2 CTAs][part_rows]
-  float4* part_o;            // [2 CTAs][D / 4][part_rows]
+  TreeCounters* counters;
+  Cut* cuts;                 // [chunks]
+  float2* part_ml;           // [2 chunks][part_rows]
+  float4* part_o;            // [2 chunks][D / 4][part_rows]
+  long long* groups;         // [CTAs][n_groups]: starts of the groups of 32 sequences (batches beyond one block)
+  int n_groups;              // groups of this call
   int part_rows;
   int* err;
   int* err_site;

@@ -20,10 +20,12 @@ struct pa_tree_handle_s {
   int max_draft = 0, words = 0, max_kv = 0;
   float scale = 0.f;
   bool bf16 = false;
-  int tile_tokens = 1, part_rows = 0;
+  int tile_tokens = 1, part_rows = 0, n_ranges = 1;
   void* ws = nullptr;
   int* err = nullptr;
+  pa::TreeCounters* counters = nullptr;
   pa::Cut* cuts = nullptr;
+  long long* groups = nullptr;
   float2* part_ml = nullptr;
   float4* part_o = nullptr;
   std::string msg = "no error";
@@ -124,6 +126,24 @@ void fill_rotary(pa::RotaryParams* p, const pa_rotary_config* rc, const uint64_t
   p->off = rc->rotary_offset;
   p->factor = rc->attention_factor;
   p->sin_sign = rc->conjugate ? -1.f : 1.f;
+}
+
+// Ranges that the line of work is cut into: with Hk chunks each they should
+// fill the SMs evenly, and few ranges leave few partial results: the fewest
+// that keep 94 % of the SMs busy, else the best of up to four rounds.
+int pick_ranges(int sms, int Hk) {
+  int best = 1;
+  double best_share = 0.0;
+  for (int n = std::max(1, sms / Hk); n <= std::max(1, 4 * sms / Hk); ++n) {
+    const int chunks = n * Hk, rounds = (chunks + sms - 1) / sms;
+    const double share = (double)chunks / (rounds * sms);
+    if (share > best_share + 1e-9) {
+      best = n;
+      best_share = share;
+    }
+    if (share >= 0.94) break;
+  }
+  return best;
 }
 
 // Arguments every paged call of a step has.
@@ -278,18 +298,21 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) e = pa::tree_configure(c.head_size, h->bf16);
-  // Workspace: error word, the cut units, and two partial results per CTA
-  // (256-byte aligned pieces).
+  // Workspace: error word, counters, the cut units, the starts of the groups
+  // of sequences (per CTA) and two partial results per chunk (256-byte
+  // aligned pieces).
   const int G = c.num_heads / c.kv_num_heads;
   h->tile_tokens = pa::kPrefillRows / G;
   h->part_rows = max_draft_tokens > h->tile_tokens ? 2 * pa::kPrefillRows : (max_draft_tokens * G + 31) / 32 * 32;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t slots = 2 * (size_t)h->num_sms, D = c.head_size;
-  const size_t o_cut = 256, o_ml = o_cut + up(sizeof(pa::Cut) * h->num_sms);
-  const size_t o_po = o_ml + up(sizeof(float2) * slots * h->part_rows);
-  const size_t ws_bytes = o_po + sizeof(float) * slots * h->part_rows * D;
+  h->n_ranges = pick_ranges(h->num_sms, c.kv_num_heads);
+  const size_t chunks = (size_t)h->n_ranges * c.kv_num_heads, D = c.head_size;
+  const size_t o_cnt = 256, o_cut = 512, o_grp = o_cut + up(sizeof(pa::Cut) * chunks);
+  const size_t o_ml = o_grp + up(sizeof(long long) * h->num_sms * ((c.max_batch + 31) / 32));
+  const size_t o_po = o_ml + up(sizeof(float2) * 2 * chunks * h->part_rows);
+  const size_t ws_bytes = o_po + sizeof(float) * 2 * chunks * h->part_rows * D;
   if (e == cudaSuccess) e = cudaMalloc(&h->ws, ws_bytes);
-  if (e == cudaSuccess) e = cudaMemset(h->ws, 0, o_ml);
+  if (e == cudaSuccess) e = cudaMemset(h->ws, 0, o_cut);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     if (h->ws) cudaFree(h->ws);
@@ -298,7 +321,9 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   }
   uint8_t* w = static_cast<uint8_t*>(h->ws);
   h->err = reinterpret_cast<int*>(w);
+  h->counters = reinterpret_cast<pa::TreeCounters*>(w + o_cnt);
   h->cuts = reinterpret_cast<pa::Cut*>(w + o_cut);
+  h->groups = reinterpret_cast<long long*>(w + o_grp);
   h->part_ml = reinterpret_cast<float2*>(w + o_ml);
   h->part_o = reinterpret_cast<float4*>(w + o_po);
   *out = h;
@@ -441,7 +466,12 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   p.log_page_rows = 0;
   while ((1 << p.log_page_rows) < page_rows) ++p.log_page_rows;
   p.oob_row = c.num_blocks * c.block_size;
-  p.min_tiles = 1;
+  p.n_ranges = h->n_ranges;
+  p.min_len = 1;
+  p.q_tiles = h->max_draft > h->tile_tokens ? 2 : 1;
+  p.counters = h->counters;
+  p.groups = h->groups;
+  p.n_groups = (batch + 31) / 32;
   p.cuts = h->cuts;
   p.part_ml = h->part_ml;
   p.part_o = h->part_o;
@@ -450,8 +480,8 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   p.err_site = h->err + 1;
   CUtensorMap tq, tk, tv;
   if (!pa::encode_rows_map(&tq, query, D, H, token_count, p.G, p.tile_tokens) ||
-      !pa::encode_rows_map(&tk, key_cache, D, Hk, (long long)c.num_blocks * c.block_size, 1, page_rows) ||
-      !pa::encode_rows_map(&tv, value_cache, D, Hk, (long long)c.num_blocks * c.block_size, 1, page_rows))
+      !pa::encode_groups_map(&tk, key_cache, D, Hk, (long long)c.num_blocks * c.block_size, page_rows) ||
+      !pa::encode_groups_map(&tv, value_cache, D, Hk, (long long)c.num_blocks * c.block_size, page_rows))
     return tree_fail(h, PA_CUDA_ERROR, "cuTensorMapEncodeTiled failed");
   cudaError_t e = pa::launch_tree(tq, tk, tv, p, h->bf16, h->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return tree_cuda_fail(h, e, "tree attention launch");

@@ -9,12 +9,16 @@
 // Partial results over ranges of keys join by out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
 //
 // Work: a unit is a sequence, a kv head and up to two 128-row tiles; its
-// length is its number of 128-key tiles.  All units in a line are cut into
-// equal ranges, one per CTA (one CTA per SM), whatever unit borders they
-// cross: every SM streams the same number of key tiles, and at most one unit
-// border per range is a cut, whose two or more partial results a second small
-// kernel joins.  Every CTA finds its range from the lengths by itself (one
-// read of the lengths, a block scan), so the step needs no planning launch.
+// length is its number of 128-key tiles plus a few that stand for its fixed
+// cost.  The units of one kv head stand in a line (the same line for every
+// head) that is cut into equal ranges, whatever unit borders they cross; a
+// chunk is a range of one head, and consecutive chunks are the heads of one
+// range, so that CTAs working at the same time read the same pool rows (one
+// row holds all heads).  A CTA (one per SM) takes one chunk, or every
+// gridDim-th.  A unit that a border cuts leaves partial results, which a
+// second small kernel joins.  Every CTA lays out the line from the lengths by
+// itself (one read of the lengths and a block scan), so the step needs no
+// planning launch.
 //
 // A unit of two row tiles runs them as two streams over the same key tiles;
 // a unit of one row tile runs its even and odd key tiles as the two streams
@@ -32,8 +36,10 @@
 //
 // Roles (384 threads): warpgroups 0 and 1, softmax and epilogue of the two
 // streams (thread = row = TMEM lane); warp 8 K/V producer (TMA, a ring of
-// slots in the order K0 V0 K1 V1 ...), warp 9 TMEM owner and MMA issuer, warp
-// 10 walks the CTA's range, publishes segments and loads Q.
+// slots in the order of their use), warp 9 TMEM owner and MMA issuer, warp
+// 10 takes chunks, publishes their segments and loads Q.
+#include <algorithm>
+
 #include "f32x2.cuh"
 #include "ptx.cuh"
 #include "step.h"
@@ -57,20 +63,27 @@ constexpr int kInfoRing = 4;  // segments published ahead of their use
 // Page masks of the K/V tiles in flight: the producer cannot be a whole ring
 // ahead of a stream (a slot is reused only after MMAs that follow the softmax
 // of all older tiles but the last few).
-constexpr int kMaskRing = 8;
+constexpr int kMaskRing = 16;
+constexpr int kMaxSlots = 12;  // K/V ring slots at most
+constexpr int kUnitCost = 2;  // a unit's fixed cost in key tiles
 
 template <int D>
 struct TreeCfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kQTileBytes = kRows * D * 2;  // [chunk][row][128 B]
-  static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V tile [chunk][key][128 B]
-  static constexpr int kSlotsFit = (kSmemLimit - kCtrlBytes - 2 * kQTileBytes) / kSlotBytes;
-  static constexpr int kSlots = kSlotsFit > 8 ? 8 : kSlotsFit;
+  static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V tile [key / 8][chunk][key % 8][128 B]
+  static constexpr int kGroupBytes = kChunks * 1024;  // its 8-key groups
+  // Slots of the K/V ring beside `q_tiles` Q tiles.
+  static __host__ __device__ constexpr int slots(int q_tiles) {
+    const int fit = (kSmemLimit - kCtrlBytes - q_tiles * kQTileBytes) / kSlotBytes;
+    return fit < kMaxSlots ? fit : kMaxSlots;
+  }
   static __host__ __device__ constexpr int s_col(int X) { return X * kKeys; }
   static __host__ __device__ constexpr int o_col(int X) { return 2 * kKeys + X * D; }
   static constexpr int kTmemCols = 512;
-  static constexpr int kDataBytes = 2 * kQTileBytes + kSlots * kSlotBytes;
-  static constexpr int kSmemBytes = kDataBytes + kCtrlBytes;
+  static __host__ __device__ constexpr int smem_bytes(int q_tiles) {
+    return q_tiles * kQTileBytes + slots(q_tiles) * kSlotBytes + kCtrlBytes;
+  }
 };
 
 // One range of a unit's key tiles.
@@ -91,21 +104,32 @@ struct Segment {
 
 struct Ctrl {
   Segment seg[kInfoRing];
-  uint32_t kv_mask[kMaskRing];    // per K/V tile (tile number mod ring): its pages that are unmapped
-  uint32_t bad[8][kTreeMaxWords];  // per softmax warp: draft tokens of the segment with non-finite V
-  float2 ml[2][kRows];            // per stream: running maximum and sum of the segment
+  float2 ml[2][kRows];                // per stream: running maximum and sum of the segment
+  uint32_t bad[2][2][kTreeMaxWords];  // per segment parity and stream: draft tokens with non-finite V
+  uint8_t kv_mask[kMaskRing];         // per K/V tile (tile number mod ring): its pages that are unmapped
   uint64_t mask_full[kMaskRing];
-  uint64_t full[8], empty[8];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t info_full[kInfoRing], info_empty[kInfoRing];
   uint64_t xchg_full, xchg_done;
   uint64_t drain;
-  long long scan[kThreads / 32];
-  long long start_off;  // this CTA's first key tile, within sequence start_b
-  int start_b;
+  long long scan[kThreads / 32];      // lengths of the first groups of 32 sequences, then where they start
+  long long total;
   uint32_t tmem_base;
   int abort;
+};
+
+// A position in the K/V ring: the slot and the phase of its barriers.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 // What the schedule needs of a sequence.
@@ -113,8 +137,8 @@ struct SeqWork {
   int past, n, t0;
   int lo;        // first key walked (a multiple of 128)
   int nt;        // key tiles of each unit
-  int pairs;     // units per kv head
-  long long len; // key tiles of all units
+  int pairs;     // units
+  long long len; // their length in the line
 };
 
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bits) {
@@ -137,7 +161,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bit
     s.lo = p.window >= 1 ? (max(0, s.past + 1 - p.window) & ~(kKeys - 1)) : 0;
     s.nt = (s.past + s.n - s.lo + kKeys - 1) / kKeys;
     s.pairs = (s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-    s.len = (long long)s.nt * s.pairs * p.Hk;
+    s.len = (long long)(s.nt + kUnitCost) * s.pairs;
   }
   return s;
 }
@@ -156,9 +180,28 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   return upto_b & ~upto_a;
 }
 
+// Bounded mbarrier wait: gives up (returns false) when another role has set
+// *abort, or after kWaitLimit polls, setting it to the wait's site.  (Small:
+// the kernel's code has to stay in the instruction cache, see the end of the
+// file's comment.)
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
+  uint32_t i = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (++i == kWaitLimit) *abort = kSiteTree | site;
+    if ((i & 1023) == 0 && *abort) return false;
+  }
+  return true;
+}
+
 template <bool BF>
 __device__ __forceinline__ bool nonfinite16(uint32_t h) {
   return BF ? (h & 0x7f80u) == 0x7f80u : (h & 0x7c00u) == 0x7c00u;
+}
+
+// Word of the segment's draft tokens with non-finite V that holds token i.
+__device__ __forceinline__ uint32_t bad_word(const Ctrl* ctl, int parity, int i) {
+  return ctl->bad[parity][0][i >> 5] | ctl->bad[parity][1][i >> 5];
 }
 
 // GEN: softcap, distance bias or a window (checked at run time); without it
@@ -168,11 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D>;
-  constexpr int S = C::kSlots;
+  const int S = C::slots(p.q_tiles);
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* q_s = smem;                       // [tile A, tile B]
-  uint8_t* kv_s = q_s + 2 * C::kQTileBytes;  // [slot]: K_i is load 2i, V_i load 2i+1
-  Ctrl* ctl = reinterpret_cast<Ctrl*>(smem + C::kDataBytes);
+  uint8_t* q_s = smem;                                // [tile A (, tile B)]
+  uint8_t* kv_s = q_s + p.q_tiles * C::kQTileBytes;  // [slot]
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(kv_s + S * C::kSlotBytes);
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -198,10 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->xchg_done, 8);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
-    ctl->start_b = -1;
     fence_mbar_init();
   }
-  if (threadIdx.x < 8 * kTreeMaxWords) ctl->bad[0][threadIdx.x] = 0;
+  if (threadIdx.x < 4 * kTreeMaxWords) ctl->bad[0][0][threadIdx.x] = 0;
   if (warp == kFetchWarp && lane == 0) prefetch_tmap(&tm_q);
   if (warp == kProducerWarp && lane == 0) {
     prefetch_tmap(&tm_k);
@@ -211,58 +253,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();  // lengths, queries and pools may come from the previous kernel
   griddep_launch_dependents();
 
-  // The line of all units: its length, and where this CTA's range starts.
+  // Where each group of 32 sequences starts in the line, and its length.
+  long long* const groups = p.batch <= kThreads ? ctl->scan : p.groups + (size_t)blockIdx.x * p.n_groups;
   int bits = 0;
-  long long total = 0;
-  SeqWork mine{};
-  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
-    const SeqWork s = seq_work(p, b, bits);
-    if (b == (int)threadIdx.x) mine = s;
-    total += s.len;
-  }
-  if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) ctl->scan[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += ctl->scan[w];
-  const long long active = min((long long)gridDim.x, (total + p.min_tiles - 1) / p.min_tiles);
-  if ((smem_u32(smem) & 1023) != 0) {  // the swizzled operands need it; never seen
-    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
-    if (threadIdx.x == 0) p.cuts[blockIdx.x].rows = 0;
-    return;
-  }
-  if (blockIdx.x >= active) {
-    if (threadIdx.x == 0) p.cuts[blockIdx.x].rows = 0;
-    return;
-  }
-  const long long r_begin = total * blockIdx.x / active, r_end = total * (blockIdx.x + 1) / active;
-  long long before = 0;  // length of the sequences of earlier rounds
+  long long before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    int ignored = 0;
-    long long len = 0;
-    if (b < p.batch) len = b0 == 0 ? mine.len : seq_work(p, b, ignored).len;
-    long long incl = len;
+    long long len = b < p.batch ? seq_work(p, b, bits).len : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
+    for (int o = 16; o > 0; o >>= 1) len += __shfl_xor_sync(0xffffffffu, len, o);
     __syncthreads();
-    if (lane == 31) ctl->scan[warp] = incl;
+    if (lane == 0) ctl->scan[warp] = len;
     __syncthreads();
-    long long first = before + incl - len;
+    long long first = before;
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) first += ctl->scan[w];
       before += ctl->scan[w];
     }
-    if (len > 0 && first <= r_begin && r_begin < first + len) {
-      ctl->start_b = b;
-      ctl->start_off = r_begin - first;
-    }
+    if (p.batch <= kThreads) __syncthreads();  // the groups' starts replace their lengths
+    if (lane == 0 && (b0 >> 5) + warp < p.n_groups) groups[(b0 >> 5) + warp] = first;
+  }
+  if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
+  if (threadIdx.x == 0) ctl->total = before;
+  if ((smem_u32(smem) & 1023) != 0) {  // the swizzled operands need it; never seen
+    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+    return;
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tmem_base, C::kTmemCols);
@@ -281,59 +296,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegControl>();
     if (warp == kFetchWarp) {
       // ---------------------------------------------------------- fetcher
-      // Walks the range, publishes its segments and loads their Q tiles once
-      // the previous segment's S products are done.
+      // Takes chunks, publishes their segments and loads a segment's Q tiles
+      // once the previous segment's S products are done.
       const uint32_t q_bytes = C::kChunks * p.G * p.tile_tokens * 128;
-      int b = ctl->start_b;
-      long long off = ctl->start_off, r = r_begin;
-      uint32_t q_loads = 0;
-      Cut cut{};  // the unit that starts in this range and goes on behind it
+      const long long total = ctl->total;
+      const int n_ranges = (int)min((long long)p.n_ranges, (total + p.min_len - 1) / p.min_len);
+      const int n_chunks = n_ranges * p.Hk;
+      // A window of 32 sequences, one per lane: where each ends in the line.
+      int group = -1;
+      long long win_lo = 0, win_hi = 0, seq_end = 0;
+      SeqWork mine{};
       int ignored = 0;
-      SeqWork s = seq_work(p, b, ignored);
+      uint32_t q_loads = 0;
+      int chunk = (int)blockIdx.x - (int)gridDim.x, range = 0;
+      long long r = 0, r_begin = 0, r_end = 0;
       for (uint32_t tt = 0;; ++tt) {
         Segment f{};
-        if (r < r_end) {
-          while (off >= s.len) {  // next sequence with work (one exists: r < total)
-            off = 0;
-            s = seq_work(p, ++b, ignored);
+        while (true) {
+          if (r >= r_end) {  // next chunk
+            chunk += gridDim.x;
+            if (chunk >= n_chunks) break;
+            range = chunk / p.Hk;
+            r = r_begin = total * range / n_ranges;
+            r_end = total * (range + 1) / n_ranges;
+            continue;
           }
-          const int u = (int)(off / s.nt), tile0 = (int)(off - (long long)u * s.nt);
-          const int pair = u % s.pairs;
+          if (r >= win_hi || r < win_lo || group < 0) {
+            int g0 = r < win_lo ? 0 : max(group, 0), at = 0;
+            for (;; g0 += 32) {
+              const int g = g0 + lane;
+              const unsigned le = __ballot_sync(0xffffffffu, g < p.n_groups && groups[min(g, p.n_groups - 1)] <= r);
+              at = __popc(le);  // groups start in order
+              if (at < 32) break;
+            }
+            group = at > 0 ? g0 + at - 1 : g0 - 1;
+            win_lo = groups[group];
+            const int b = 32 * group + lane;
+            mine = SeqWork{};
+            if (b < p.batch) mine = seq_work(p, b, ignored);
+            seq_end = mine.len;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long up = __shfl_up_sync(0xffffffffu, seq_end, o);
+              if (lane >= o) seq_end += up;
+            }
+            seq_end += win_lo;
+            win_hi = __shfl_sync(0xffffffffu, seq_end, 31);
+          }
+          const int src = __ffs(__ballot_sync(0xffffffffu, r < seq_end)) - 1;
+          SeqWork s;
+          s.past = __shfl_sync(0xffffffffu, mine.past, src);
+          s.n = __shfl_sync(0xffffffffu, mine.n, src);
+          s.t0 = __shfl_sync(0xffffffffu, mine.t0, src);
+          s.lo = __shfl_sync(0xffffffffu, mine.lo, src);
+          s.nt = __shfl_sync(0xffffffffu, mine.nt, src);
+          const long long off = r - __shfl_sync(0xffffffffu, seq_end - mine.len, src);
+          const int u = (int)(off / (s.nt + kUnitCost)), tile0 = (int)(off - (long long)u * (s.nt + kUnitCost));
+          if (tile0 >= s.nt) {  // the unit's fixed cost
+            r += s.nt + kUnitCost - tile0;
+            continue;
+          }
           f.live = 1;
-          f.b = b;
-          f.k = u / s.pairs;
-          f.t0 = s.t0 + pair * 2 * p.tile_tokens;
-          f.ntok = min(2 * p.tile_tokens, s.n - pair * 2 * p.tile_tokens);
+          f.b = 32 * group + src;
+          f.k = chunk % p.Hk;
+          f.t0 = s.t0 + u * 2 * p.tile_tokens;
+          f.ntok = min(2 * p.tile_tokens, s.n - u * 2 * p.tile_tokens);
           f.two = f.ntok > p.tile_tokens;
           f.seq_t0 = s.t0;
           f.n = s.n;
           f.past = s.past;
           f.key0 = s.lo + tile0 * kKeys;
           f.nt = (int)min((long long)(s.nt - tile0), r_end - r);
-          f.slot = f.nt == s.nt ? -1 : 2 * (int)blockIdx.x + (r == r_begin ? 0 : 1);
-          if (tile0 == 0 && f.nt < s.nt) {
-            // the CTA that holds the unit's last tile: the largest c with total * c / active <= last
-            const long long last = r + s.nt - 1;
+          f.slot = f.nt == s.nt ? -1 : 2 * chunk + (r == r_begin ? 0 : 1);
+          if (tile0 == 0 && f.nt < s.nt && lane == 0) {  // the unit goes on in later ranges
+            Cut cut{};
             cut.rows = f.two ? kRows + (f.ntok - p.tile_tokens) * p.G : f.ntok * p.G;
             cut.slot0 = f.slot;
-            cut.more = (int)(((last + 1) * active - 1) / total) - (int)blockIdx.x;
+            cut.slot1 = 2 * (chunk + p.Hk);
+            // the range that holds the unit's last tile: the largest i with total * i / n_ranges <= last
+            cut.more = (int)(((r + s.nt) * n_ranges - 1) / total) - range;
             cut.t0 = f.t0;
             cut.ntok = f.ntok;
             cut.k = f.k;
+            p.cuts[atomicAdd(&p.counters->n_cuts, 1)] = cut;
           }
-          off += f.nt;
           r += f.nt;
+          break;
         }
         const int slot = tt % kInfoRing;
         bool ok = true;
         if (lane == 0) {
-          if (!wait_or_abort(&ctl->info_empty[slot], ((tt / kInfoRing) & 1) ^ 1, abort, p.err, p.err_site, kSiteTree | 1)) {
+          if (!tree_wait(&ctl->info_empty[slot], ((tt / kInfoRing) & 1) ^ 1, abort, 1)) {
             ok = false;
           } else {
             ctl->seg[slot] = f;
             mbar_arrive(&ctl->info_full[slot]);
             if (f.live) {
-              if (!wait_or_abort(&ctl->q_empty, (tt & 1) ^ 1, abort, p.err, p.err_site, kSiteTree | 2)) {
+              if (!tree_wait(&ctl->q_empty, (tt & 1) ^ 1, abort, 2)) {
                 ok = false;
               } else {
                 mbar_arrive_expect_tx(&ctl->q_full, (f.two ? 2 : 1) * q_bytes);
@@ -349,49 +408,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok || !f.live) break;
       }
-      if (lane == 0) {
-        p.cuts[blockIdx.x] = cut;
-        if (*abort && q_loads > 0) {
-          // Gave up: let the copies already issued land before the CTA exits.
-          for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&ctl->q_full, (q_loads - 1) & 1); ++i) {
-          }
+      if (lane == 0 && *abort && q_loads > 0) {
+        // Gave up: let the copies already issued land before the CTA exits.
+        for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&ctl->q_full, (q_loads - 1) & 1); ++i) {
         }
       }
     } else if (warp == kProducerWarp) {
       // ----------------------------------------------------- K/V producer
-      uint32_t n_loads = 0;  // K/V slot loads issued so far
+      uint32_t n_loads = 0, n_tiles = 0;  // K/V slot loads and key tiles issued so far
+      RingPos at;
       bool ok = true;
-      // One K or V tile into the next ring slot: lane l copies page
-      // l / chunks, 64-column chunk l % chunks (a box of {64, 1, page rows}).
-      auto load_tile = [&](const CUtensorMap* tm, int k, int rc, bool is_v, uint32_t mask) -> bool {
-        const int slot = n_loads % S;
-        if (lane == 0) {
-          if (!wait_or_abort(&ctl->empty[slot], ((n_loads / S) & 1) ^ 1, abort, p.err, p.err_site, kSiteTree | 3)) {
-            ok = false;
-          } else {
-            if (!is_v) {
-              ctl->kv_mask[(n_loads >> 1) % kMaskRing] = mask;
-              mbar_arrive(&ctl->mask_full[(n_loads >> 1) % kMaskRing]);
-            }
-            mbar_arrive_expect_tx(&ctl->full[slot], C::kSlotBytes);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) return false;
-        const int lp = lane / C::kChunks, lc = lane % C::kChunks;
-        const int prc = __shfl_sync(0xffffffffu, rc, lp & 31);
-        if (lp < pages) {
-          uint8_t* dst = kv_s + slot * C::kSlotBytes + lc * (kKeys * 128) + ((uint32_t)lp << (log_r + 7));
-          tma_load_3d(dst, tm, lc * 64, k, prc, &ctl->full[slot]);
-        }
-        ++n_loads;
-        return true;
-      };
       for (uint32_t tt = 0; ok; ++tt) {
         const int slot = tt % kInfoRing;
         int got = 1;
         if (lane == 0)
-          got = wait_or_abort(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, p.err, p.err_site, kSiteTree | 4);
+          got = tree_wait(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, 4);
         if (!__shfl_sync(0xffffffffu, got, 0)) break;
         const Segment cur = ctl->seg[slot];
         if (!cur.live) break;
@@ -401,23 +432,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           return (e < p.MB && ((long long)e << p.log_bs) < end) ? bt_row[e] : -1;
         };
         int win = cur.key0 >> p.log_bs;
-        int id = load_id(win + lane);
-        for (int i = 0; i < cur.nt; ++i) {
-          const int key0 = cur.key0 + i * kKeys;
-          if (((key0 + kKeys - 1) >> p.log_bs) >= win + 32) {
-            win = key0 >> p.log_bs;
-            id = load_id(win + lane);
+        int id = load_id(win + lane), rc = p.oob_row, rc_before = 0;
+        // In the order of use (see the MMA issuer): K_i V_i with two row
+        // tiles, K_i V_{i-1} with one.
+        const int lag = cur.two ? 0 : 1;
+#pragma unroll 1
+        for (int l = 0; l < 2 * (cur.nt + lag) && ok; ++l) {
+          const bool is_v = l & 1;
+          const int i = l >> 1;
+          uint32_t mask = 0;
+          if (is_v ? i < lag : i >= cur.nt) continue;
+          if (!is_v) {  // the tile's pages
+            const int key0 = cur.key0 + i * kKeys;
+            if (((key0 + kKeys - 1) >> p.log_bs) >= win + 32) {
+              win = key0 >> p.log_bs;
+              id = load_id(win + lane);
+            }
+            const int pos = key0 + (lane << log_r);
+            const int idx = (pos >> p.log_bs) - win;
+            const int blk = __shfl_sync(0xffffffffu, id, idx & 31);
+            rc_before = rc;
+            rc = p.oob_row;
+            if (lane < pages && pos < end) {
+              if (blk >= 0 && blk < p.NB) rc = (blk << p.log_bs) + (pos & (p.bs - 1));
+              else if (blk != -1) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+            }
+            mask = __ballot_sync(0xffffffffu, lane < pages && rc == p.oob_row);
           }
-          const int pos = key0 + (lane << log_r);
-          const int idx = (pos >> p.log_bs) - win;
-          const int blk = __shfl_sync(0xffffffffu, id, idx & 31);
-          int rc = p.oob_row;
-          if (lane < pages && pos < end) {
-            if (blk >= 0 && blk < p.NB) rc = (blk << p.log_bs) + (pos & (p.bs - 1));
-            else if (blk != -1) atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+          // Into the next ring slot: lane l copies page l.
+          if (lane == 0) {
+            if (!tree_wait(&ctl->empty[at.slot], at.phase ^ 1, abort, 3)) {
+              ok = false;
+            } else {
+              if (!is_v) {
+                ctl->kv_mask[n_tiles % kMaskRing] = (uint8_t)mask;
+                mbar_arrive(&ctl->mask_full[n_tiles % kMaskRing]);
+              }
+              mbar_arrive_expect_tx(&ctl->full[at.slot], C::kSlotBytes);
+            }
           }
-          const uint32_t mask = __ballot_sync(0xffffffffu, lane < pages && rc == p.oob_row);
-          if (!load_tile(&tm_k, cur.k, rc, false, mask) || !load_tile(&tm_v, cur.k, rc, true, 0)) break;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const int row = is_v && lag && i < cur.nt ? rc_before : rc;
+          if (lane < pages)
+            tma_load_5d(kv_s + at.slot * C::kSlotBytes + (lane << (log_r - 3)) * C::kGroupBytes, is_v ? &tm_v : &tm_k, 0,
+                        0, 0, row >> 3, cur.k, &ctl->full[at.slot]);
+          ++n_loads;
+          n_tiles += is_v ? 0 : 1;
+          at.next(S);
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(&ctl->info_empty[slot]);
@@ -435,17 +497,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // is stream j & 1 and key tile j / 2 (two row tiles) or j (one).  In
       // issue order S(0) S(1) PV(0) S(2) PV(1) S(3) ...: S(j + 2) may
       // overwrite P(j)'s columns because MMAs of one thread complete in order,
-      // and a wait on S(j + 2) covers PV(j).
+      // and a wait on S(j + 2) covers PV(j).  First uses of tiles: with two
+      // row tiles K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 K3 ... (the ring's
+      // order, so that a slot is free as soon as it is the next to be filled).
       constexpr uint32_t idesc_s = umma_idesc_f16(kRows, kKeys, 0, 0, BF ? 1 : 0);
       constexpr uint32_t idesc_o = umma_idesc_f16(kRows, D, 0, 1, BF ? 1 : 0);
-      const uint64_t desc_k = smem_desc_sw128(0, 16, 1024);           // K-major Q and K, + (address >> 4)
-      const uint64_t desc_v = smem_desc_sw128(0, kKeys * 128, 1024);  // MN-major V, + (address >> 4)
+      const uint64_t desc_q = smem_desc_sw128(0, 16, 1024);                // K-major Q, + (address >> 4)
+      const uint64_t desc_k = smem_desc_sw128(0, 16, C::kGroupBytes);      // K-major K
+      const uint64_t desc_v = smem_desc_sw128(0, 1024, C::kGroupBytes);    // MN-major V
       const uint32_t kv_addr = smem_u32(kv_s), q_addr = smem_u32(q_s);
       const bool leader = elect_one();
       auto wait_bar = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return wait_or_abort(bar, parity, abort, p.err, p.err_site, kSiteTree | 5);
+        return tree_wait(bar, parity, abort, 5);
       };
-      uint32_t g = 0, pcnt[2] = {0, 0};
+      uint32_t pcnt = 0;  // bit X: parity of p_full[X]
+      RingPos at;
+      int k_slot = 0, v_slot = 0;  // slots that the second row tile uses again
       bool ok = leader;
       for (uint32_t tt = 0; ok; ++tt) {
         const int slot = tt % kInfoRing;
@@ -453,46 +520,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Segment& sg = ctl->seg[slot];
         if (!sg.live) break;
         const int two = sg.two, nt = sg.nt, jobs = two ? 2 * nt : nt;
-        auto issue_s = [&](int j) -> bool {
-          const int X = j & 1, i = two ? j >> 1 : j;
-          const uint32_t n = 2 * (g + i);
-          const int st = n % S;
-          if (j == 0 && !wait_bar(&ctl->q_full, tt & 1)) return false;
-          if ((!two || X == 0) && !wait_bar(&ctl->full[st], (n / S) & 1)) return false;
-          tc_fence_after();
-          const uint64_t a0 = desc_k + ((q_addr + (two ? X : 0) * C::kQTileBytes) >> 4);
-          const uint64_t b0 = desc_k + ((kv_addr + st * C::kSlotBytes) >> 4);
+#pragma unroll 1
+        for (int j = 0; j < jobs + 2 && ok; ++j) {
+          const int X = j & 1;
+          if (j >= 2) {  // O_X += P_X V of job j - 2
+            // its P; the segment's first PV of the stream overwrites O_X, which the last segment has read
+            ok = wait_bar(&ctl->p_full[X], (pcnt >> X) & 1) &&
+                 (j >= 4 || tt == 0 || wait_bar(&ctl->o_free[X], (tt - 1) & 1));
+            if (!ok) break;
+            pcnt ^= 1u << X;
+            if (!two || X == 0) {
+              if (!(ok = wait_bar(&ctl->full[at.slot], at.phase))) break;
+              v_slot = at.slot;
+              at.next(S);
+            }
+            tc_fence_after();
+            const uint64_t b0 = desc_v + ((kv_addr + v_slot * C::kSlotBytes) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_f16(tmem + C::s_col(X), a0 + (((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4),
-                     b0 + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
-          umma_commit(&ctl->s_full[X]);
-          if (!two || X == 1) umma_commit(&ctl->empty[st]);
-          if (j == jobs - 1) umma_commit(&ctl->q_empty);
-          return true;
-        };
-        auto issue_pv = [&](int j) -> bool {
-          const int X = j & 1, i = two ? j >> 1 : j;
-          if (!wait_bar(&ctl->p_full[X], pcnt[X] & 1)) return false;
-          ++pcnt[X];
-          // the segment's first PV of the stream overwrites O_X: the last segment's has been read
-          if (j < 2 && tt > 0 && !wait_bar(&ctl->o_free[X], (tt - 1) & 1)) return false;
-          const uint32_t n = 2 * (g + i) + 1;
-          const int st = n % S;
-          if ((!two || X == 0) && !wait_bar(&ctl->full[st], (n / S) & 1)) return false;
-          tc_fence_after();
-          const uint64_t b0 = desc_v + ((kv_addr + st * C::kSlotBytes) >> 4);
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_f16_ts(tmem + C::o_col(0) + X * D, tmem + X * kKeys + kk * 8, b0 + ((kk * 2 * C::kGroupBytes) >> 4), idesc_o,
+                          (j > 3 || kk > 0) ? 1u : 0u);
+            if (!two || X == 1) umma_commit(&ctl->empty[v_slot]);
+            if (j >= jobs) umma_commit(&ctl->o_done[X]);
+          }
+          if (j < jobs) {  // S_X = Q K^T of job j
+            if (j == 0 && !(ok = wait_bar(&ctl->q_full, tt & 1))) break;
+            if (!two || X == 0) {
+              if (!(ok = wait_bar(&ctl->full[at.slot], at.phase))) break;
+              k_slot = at.slot;
+              at.next(S);
+            }
+            tc_fence_after();
+            const uint64_t a0 = desc_q + ((q_addr + (two ? X : 0) * C::kQTileBytes) >> 4);
+            const uint64_t b0 = desc_k + ((kv_addr + k_slot * C::kSlotBytes) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_f16_ts(tmem + C::o_col(X), tmem + C::s_col(X) + kk * 8, b0 + ((kk * 16 * 128) >> 4), idesc_o,
-                        (j > 1 || kk > 0) ? 1u : 0u);
-          if (!two || X == 1) umma_commit(&ctl->empty[st]);
-          if (j >= jobs - 2) umma_commit(&ctl->o_done[X]);
-          return true;
-        };
-        ok = issue_s(0) && (jobs == 1 || issue_s(1));
-        for (int j = 0; j < jobs && ok; ++j) ok = issue_pv(j) && (j + 2 >= jobs || issue_s(j + 2));
-        g += nt;
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_f16(tmem + X * kKeys, a0 + (((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4),
+                       b0 + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+            umma_commit(&ctl->s_full[X]);
+            if (!two || X == 1) umma_commit(&ctl->empty[k_slot]);
+            if (j == jobs - 1) umma_commit(&ctl->q_empty);
+          }
+        }
         if (!ok) break;
         mbar_arrive(&ctl->info_empty[slot]);
       }
@@ -511,16 +580,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;    // row of the tile == TMEM lane
     const int rj = r / p.G;             // its token within the tile
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float mul = GEN ? 1.f : p.scale * kLog2e;
+    const float mul = GEN && (p.softcap > 0.f || p.slopes) ? 1.f : p.scale * kLog2e;
     uint32_t g = 0, scnt = 0, ocnt[2] = {0, 0};
+    RingPos ring;  // of the segment's first load
     float x[kKeys];
     for (uint32_t tt = 0;; ++tt) {
       const int slot = tt % kInfoRing;
-      if (!wait_or_abort(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, p.err, p.err_site, kSiteTree | 6)) break;
+      if (!tree_wait(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, 6)) break;
       const Segment& sg = ctl->seg[slot];
       if (!sg.live) break;
       // the exchange of the last segment has been read by both streams
-      if (tt > 0 && !wait_or_abort(&ctl->xchg_done, (tt - 1) & 1, abort, p.err, p.err_site, kSiteTree | 7)) break;
+      if (tt > 0) {
+        if (!tree_wait(&ctl->xchg_done, (tt - 1) & 1, abort, 7)) break;
+        if ((warp & 3) == 0 && lane < kTreeMaxWords) ctl->bad[(tt - 1) & 1][X][lane] = 0;
+      }
       const int two = sg.two, nt = sg.nt, past = sg.past, n = sg.n;
       const int jt = (two ? X * p.tile_tokens : 0) + rj;  // the row's token within the unit
       const bool row_ok = rj < p.tile_tokens && jt < sg.ntok;
@@ -535,21 +608,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.slopes && row_ok) slope2 = p.slopes[sg.k * p.G + (r - rj * p.G)] * kLog2e;
       }
       const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;  // no row admits a key below
+      if (p.mask && row_ok && sg.key0 + nt * kKeys > past) {
+        // the row's mask words, towards L1 for the tiles that hold draft tokens
+        const uint32_t* row = p.mask + (size_t)t * p.words;
+        prefetch_l1(row);
+        prefetch_l1(row + p.words - 1);
+      }
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int i = two ? 0 : X; i < nt; i += two ? 1 : 2) {
-        const uint32_t nv = 2 * (g + i) + 1, tile = g + i;
-        const int sv = nv % S;
+        const uint32_t tile = g + i;
         const int key0 = sg.key0 + i * kKeys;
         // (published before the tile's K load: read before the wait for S,
         // which hides the shared-memory load)
-        if (!wait_or_abort(&ctl->mask_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort, p.err, p.err_site,
-                           kSiteTree | 8)) {
+        if (!tree_wait(&ctl->mask_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort, 8)) {
           ok = false;
           break;
         }
         const uint32_t pmask = ctl->kv_mask[tile % kMaskRing];
-        if (!wait_or_abort(&ctl->s_full[X], scnt & 1, abort, p.err, p.err_site, kSiteTree | 9)) {
+        // A tile that is not admitted as a whole: one bit per key of this row
+        // (made before the wait for S).
+        const bool partial = key0 + kKeys > past || pmask != 0 || __any_sync(0xffffffffu, key0 < lo_row || !row_ok);
+        const bool drafts = key0 + kKeys > past;
+        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+        float kpf[4];  // GEN: lane e, entry q: position of key 32 q + e, less past
+        if constexpr (GEN) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) kpf[q] = (float)(key0 + 32 * q + lane - past);
+        }
+        if (partial && warp_ok) {
+          int kp[4];
+          if constexpr (GEN) {
+            if (drafts && p.positions) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int d = key0 + 32 * q + lane - past;
+                kp[q] = d >= 0 && d < n ? p.positions[sg.seq_t0 + d] : past + d;
+                kpf[q] = (float)(kp[q] - past);
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int k0 = key0 + 32 * q, d0 = k0 - past;  // d0: draft index of bit 0
+            uint32_t m = bit_range(lo_row - k0, -d0);
+            if (d0 + 32 > 0 && d0 < n) {
+              uint32_t md = bit_range(-d0, n - d0);
+              if (p.mask) {
+                const uint32_t* row = p.mask + (size_t)t * p.words;
+                const int wi = d0 >> 5;  // (floor)
+                const uint32_t a = wi >= 0 ? row[wi] : 0u;
+                const uint32_t b = wi + 1 < p.words ? row[wi + 1] : 0u;
+                md &= __funnelshift_r(a, b, d0 & 31);
+              } else {
+                md &= bit_range(0, j_seq + 1 - d0);
+              }
+              if constexpr (GEN) {
+                if (p.window >= 1) {
+                  uint32_t in = 0;
+                  if (p.positions) {
+#pragma unroll 1
+                    for (int e = 0; e < 32; ++e) in |= (__shfl_sync(0xffffffffu, kp[q], e) >= lo_row ? 1u : 0u) << e;
+                  } else {
+                    in = bit_range(lo_row - k0, 32);
+                  }
+                  md &= in;
+                }
+              }
+              m |= md;
+            }
+            w[q] = row_ok ? m : 0u;
+          }
+          if (pmask != 0) {
+#pragma unroll 1
+            for (int g2 = 0; g2 < pages; ++g2) {
+              if (!((pmask >> g2) & 1)) continue;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) w[q] &= ~bit_range((g2 << log_r) - 32 * q, ((g2 + 1) << log_r) - 32 * q);
+            }
+          }
+        }
+        if (!tree_wait(&ctl->s_full[X], scnt & 1, abort, 9)) {
           ok = false;
           break;
         }
@@ -562,69 +701,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           if constexpr (GEN) {
             if (p.softcap > 0.f) {
-              // c tanh(y) = c (1 - 2 / (1 + e^{2y})), in log2 units
+              // c tanh(y) = c (1 - 2 / (1 + e^{2y})), in log2 units (the
+              // approximate reciprocal is off by 2^-23 of a term below 2 c)
               const float in = 2.f * kLog2e * p.scale / p.softcap, out = p.softcap * kLog2e;
 #pragma unroll
-              for (int c = 0; c < kKeys; ++c) x[c] = fmaf(-2.f * out, __frcp_rn(1.f + ex2(x[c] * in)), out);
-            } else {
-              const float in = p.scale * kLog2e;
-#pragma unroll
-              for (int c = 0; c < kKeys; ++c) x[c] *= in;
+              for (int c = 0; c < kKeys; ++c) x[c] = fmaf(-2.f * out, rcp(1.f + ex2(x[c] * in)), out);
             }
             if (p.slopes) {
-              const float base = (float)((long long)key0 - qpos);
-              if (key0 + kKeys <= past || !p.positions) {
+              const float unit = p.softcap > 0.f ? 1.f : p.scale * kLog2e, base = slope2 * (float)(past - qpos);
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) x[c] = fmaf(slope2, base + (float)c, x[c]);
-              } else {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) {
-                  const int d = key0 + c - past;  // draft index
-                  const float gap = d < 0 || d >= n ? base + (float)c
-                                                    : (float)((long long)p.positions[sg.seq_t0 + d] - qpos);
-                  x[c] = fmaf(slope2, gap, x[c]);
-                }
-              }
+              for (int c = 0; c < kKeys; ++c)
+                x[c] = fmaf(x[c], unit, fmaf(slope2, __shfl_sync(0xffffffffu, kpf[c >> 5], c & 31), base));
             }
           }
-          if (key0 + kKeys > past || key0 < lo_row || pmask != 0 || !row_ok) {
+          if (partial) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int k0 = key0 + 32 * q;
-              uint32_t w = 0;
-              if (row_ok) {
-                w = bit_range(lo_row - k0, past - k0);
-                const int d0 = k0 - past;  // draft index of bit 0
-                if (d0 + 32 > 0 && d0 < n) {
-                  uint32_t w2;
-                  if (p.mask) {
-                    const uint32_t* row = p.mask + (size_t)t * p.words;
-                    const int wi = d0 >> 5;  // (floor)
-                    const uint32_t a = wi >= 0 && wi < p.words ? row[wi] : 0u;
-                    const uint32_t b = wi + 1 >= 0 && wi + 1 < p.words ? row[wi + 1] : 0u;
-                    w2 = __funnelshift_r(a, b, d0 & 31);
-                  } else {
-                    w2 = bit_range(0, j_seq + 1 - d0);
-                  }
-                  w2 &= bit_range(-d0, n - d0);
-                  if constexpr (GEN) {
-                    if (p.window >= 1) {
-                      for (int e = max(0, -d0); e < min(32, n - d0); ++e) {
-                        const int kpos = p.positions ? p.positions[sg.seq_t0 + d0 + e] : past + d0 + e;
-                        if (kpos < lo_row) w2 &= ~(1u << e);
-                      }
-                    }
-                  }
-                  w |= w2;
-                }
-                if (pmask != 0) {
-                  for (int g2 = 0; g2 < pages; ++g2)
-                    if ((pmask >> g2) & 1) w &= ~bit_range((g2 << log_r) - 32 * q, ((g2 + 1) << log_r) - 32 * q);
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[32 * q + e] = ((w >> e) & 1) ? x[32 * q + e] : -INFINITY;
-            }
+            for (int c = 0; c < kKeys; ++c) x[c] = ((w[c >> 5] >> (c & 31)) & 1) ? x[c] : -INFINITY;
           }
           const float cand = max_tree<kKeys>(x) * mul;
           float alpha = 1.f;
@@ -668,20 +760,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Zero V rows that no row admits by position, take non-finite values
         // out of draft rows (once per tile: stream 0 when both use it).
+        // Unmapped pages and pages behind the sequence are zero already.
         if ((key0 + kKeys > past || key0 < lo_min) && (!two || X == 0)) {
-          uint8_t* vs = kv_s + sv * C::kSlotBytes;
-          if (!wait_or_abort(&ctl->full[sv], (nv / S) & 1, abort, p.err, p.err_site, kSiteTree | 10)) {
+          // the tile's V load, counted from the segment's first, in the ring's order
+          const int n_v = two ? 2 * i + 1 : (i == nt - 1 ? 2 * i + 1 : 2 * i + 2);
+          const int turn = ring.slot + n_v, sv = turn % S;
+          if (!tree_wait(&ctl->full[sv], ring.phase ^ ((turn / S) & 1), abort, 10)) {
             ok = false;
             break;
           }
-          for (int idx = r; idx < kKeys * C::kChunks * 8; idx += 128) {
-            const int kr = idx / (C::kChunks * 8), rem = idx % (C::kChunks * 8);
-            const int pos = key0 + kr;
-            uint4* at = reinterpret_cast<uint4*>(vs + (rem >> 3) * (kKeys * 128) + kr * 128 +
-                                                 (((rem & 7) ^ (kr & 7)) << 4));
-            if (pos >= past + n || pos < lo_min) {
+          uint8_t* vs = kv_s + sv * C::kSlotBytes;
+          const int page_rows = 1 << log_r;
+          const int k_lo = min(max(lo_min - key0, 0), kKeys);                        // rows below: zero
+          const int k_draft = max(past - key0, 0);                                   // draft rows
+          const int k_end = max(past + n - key0, 0);                                 // rows from here on: zero
+          const int k_page = min((k_end + page_rows - 1) & ~(page_rows - 1), kKeys);  // ... up to here
+          constexpr int kVecs = C::kChunks * 8;  // 16-byte vectors of a row
+          auto vec_at = [&](int kr, int v) {
+            return reinterpret_cast<uint4*>(vs + (kr >> 3) * C::kGroupBytes + (v >> 3) * 1024 + (kr & 7) * 128 +
+                                            (((v & 7) ^ (kr & 7)) << 4));
+          };
+#pragma unroll 1
+          for (int idx = r; idx < k_lo * kVecs; idx += kRows) *vec_at(idx / kVecs, idx % kVecs) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int idx = k_draft * kVecs + r; idx < k_page * kVecs; idx += kRows) {
+            const int kr = idx / kVecs;
+            uint4* at = vec_at(kr, idx % kVecs);
+            if (kr >= k_end) {
               *at = make_uint4(0, 0, 0, 0);
-            } else if (pos >= past) {
+            } else if (kr >= k_lo) {
               const uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
               bool any = false;
@@ -691,8 +798,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nonfinite16<BF>(w[e] >> 16)) { w[e] &= 0x0000ffffu; any = true; }
               }
               if (any) {
+                const int d = key0 + kr - past;
                 *at = make_uint4(w[0], w[1], w[2], w[3]);
-                atomicOr(&ctl->bad[warp][(pos - past) >> 5], 1u << ((pos - past) & 31));
+                atomicOr(&ctl->bad[tt & 1][X][d >> 5], 1u << (d & 31));
               }
             }
           }
@@ -710,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ctl->ml[X][r] = make_float2(m_ref, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->xchg_full);
-      if (!wait_or_abort(&ctl->xchg_full, tt & 1, abort, p.err, p.err_site, kSiteTree | 11)) break;
+      if (!tree_wait(&ctl->xchg_full, tt & 1, abort, 11)) break;
       float f0 = 1.f, f1 = 1.f;  // factors of O_0 and O_1 (one row tile)
       if (!two) {
         const float2 a = ctl->ml[0][r], b = ctl->ml[1][r];
@@ -719,28 +827,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 = b.x == -INFINITY ? 0.f : ex2(b.x - m_ref);
         l = (f0 == 0.f ? 0.f : f0 * a.y) + (f1 == 0.f ? 0.f : f1 * b.y);
       }
-      uint32_t bad[kTreeMaxWords], any_bad = 0;
-#pragma unroll
-      for (int q = 0; q < kTreeMaxWords; ++q) {
-        bad[q] = 0;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) bad[q] |= ctl->bad[w][q];
-        any_bad |= bad[q];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->xchg_done);
-      if (any_bad) {
-        // cleared for the next segment once both streams have read it
-        if (!wait_or_abort(&ctl->xchg_done, tt & 1, abort, p.err, p.err_site, kSiteTree | 12)) break;
-        if (lane < kTreeMaxWords) ctl->bad[warp][lane] = 0;
-        __syncwarp();
-      }
+      uint32_t any_bad = lane < kTreeMaxWords ? bad_word(ctl, tt & 1, 32 * lane) : 0u;
+      any_bad = __any_sync(0xffffffffu, any_bad != 0);
+      const bool keep_bad = any_bad != 0;  // read again after the stores: released there
+      if (lane == 0 && !keep_bad) mbar_arrive(&ctl->xchg_done);
       const int jobs = two ? 2 * nt : nt;
       bool have[2] = {true, jobs >= 2};
       for (int Y = 0; Y < 2 && ok; ++Y) {
         if (!have[Y]) continue;
         if ((!two || Y == X) &&
-            !wait_or_abort(&ctl->o_done[Y], ocnt[Y] & 1, abort, p.err, p.err_site, kSiteTree | 13))
+            !tree_wait(&ctl->o_done[Y], ocnt[Y] & 1, abort, 13))
           ok = false;
         ++ocnt[Y];
       }
@@ -757,128 +853,157 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sg.slot >= 0 && row_ok && (two || X == 0)) p.part_ml[(size_t)sg.slot * p.part_rows + row] = make_float2(m_ref, l);
       __half* dst = p.out + ((size_t)t * p.H + h) * D;
       float4* part = sg.slot >= 0 ? p.part_o + (size_t)sg.slot * (D / 4) * p.part_rows + row : nullptr;
-      // two row tiles: every channel of the own O; one: half the channels of both
-      const int c0 = two ? 0 : X * (D / 64), c1 = two ? D / 32 : (X + 1) * (D / 64);
+      // Two row tiles: every channel of the own O; one: half the channels of both.
+      const int c0 = two ? 0 : X * (D / 2), c1 = two ? D : c0 + D / 2;
       if (warp_ok) {
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          float o[32];
-          tmem_ld32(lane_addr + C::o_col(two ? X : 0) + 32 * c, o);
+        for (int c = c0; c < c1; c += 32) {
+          tmem_ld32(lane_addr + C::o_col(0) + (two ? X * D : 0) + c, x);
+          if (have[1] && !two) tmem_ld32(lane_addr + C::o_col(1) + c, x + 32);
+          tmem_ld_wait();
           if (!two) {
-            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = f0 == 0.f ? 0.f : o[e] * f0;
-            if (have[1]) {
-              tmem_ld32(lane_addr + C::o_col(1) + 32 * c, x);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = f1 == 0.f ? o[e] : fmaf(x[e], f1, o[e]);
-            }
-          } else {
-            tmem_ld_wait();
-          }
-          if (any_bad && row_ok) {
-            for (int i = 0; i < n; ++i) {
-              if (!((bad[i >> 5] >> (i & 31)) & 1) || !mask_bit(p, t, j_seq, i)) continue;
-              if constexpr (GEN) {
-                const int kpos = p.positions ? p.positions[sg.seq_t0 + i] : past + i;
-                if (p.window >= 1 && kpos < lo_row) continue;
-              }
-              const int pos = past + i;
-              const int blk = p.block_table[(size_t)sg.b * p.MB + (pos >> p.log_bs)];
-              if (blk < 0 || blk >= p.NB) continue;
-              const __half* v = p.value_cache +
-                                ((((size_t)blk << p.log_bs) + (pos & (p.bs - 1))) * p.Hk + sg.k) * D + 32 * c;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (nonfinite16<BF>(__half_as_ushort(v[e]))) o[e] += elem16_to_float(v[e], BF);
+            for (int e = 0; e < 32; ++e) {
+              x[e] = f0 == 0.f ? 0.f : x[e] * f0;
+              if (f1 != 0.f) x[e] = fmaf(x[32 + e], f1, x[e]);
             }
           }
           if (row_ok) {
             if (part) {
+              float4* at = part + (size_t)(c / 4) * p.part_rows;
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                part[(size_t)(8 * c + q) * p.part_rows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              for (int q = 0; q < 8; ++q, at += p.part_rows) *at = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             } else {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint4 w;
-                w.x = pack2<BF>(o[8 * q + 0] * inv, o[8 * q + 1] * inv);
-                w.y = pack2<BF>(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
-                w.z = pack2<BF>(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
-                w.w = pack2<BF>(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
-                *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = w;
-              }
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dst + c + 8 * q) =
+                    make_uint4(pack2<BF>(x[8 * q] * inv, x[8 * q + 1] * inv), pack2<BF>(x[8 * q + 2] * inv, x[8 * q + 3] * inv),
+                               pack2<BF>(x[8 * q + 4] * inv, x[8 * q + 5] * inv),
+                               pack2<BF>(x[8 * q + 6] * inv, x[8 * q + 7] * inv));
             }
           }
         }
       }
+      // O may be overwritten by the next segment's first PV
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&ctl->o_free[0]);
         mbar_arrive(&ctl->o_free[1]);
-        mbar_arrive(&ctl->info_empty[slot]);
       }
+      if (any_bad && row_ok) {
+        // Draft keys with non-finite V: added, element by element, to what
+        // this thread has just stored for its row if the row admits them.
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          if (!((bad_word(ctl, tt & 1, i) >> (i & 31)) & 1) || !mask_bit(p, t, j_seq, i)) continue;
+          const int pos = past + i;
+          if (GEN && p.window >= 1 && (p.positions ? p.positions[sg.seq_t0 + i] : pos) < lo_row) continue;
+          const int blk = p.block_table[(size_t)sg.b * p.MB + (pos >> p.log_bs)];
+          if (blk < 0 || blk >= p.NB) continue;
+          const __half* v =
+              p.value_cache + ((((size_t)blk << p.log_bs) + (pos & (p.bs - 1))) * p.Hk + sg.k) * D;
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            if (!nonfinite16<BF>(__half_as_ushort(v[c]))) continue;
+            const float add = elem16_to_float(v[c], BF);
+            if (part) reinterpret_cast<float*>(part + (size_t)(c / 4) * p.part_rows)[c & 3] += add;
+            else dst[c] = float_to_elem16(elem16_to_float(dst[c], BF) + add, BF);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && keep_bad) mbar_arrive(&ctl->xchg_done);
+      const int turn = ring.slot + 2 * nt;
+      ring.phase ^= (turn / S) & 1;
+      ring.slot = turn % S;
+      if (lane == 0) mbar_arrive(&ctl->info_empty[slot]);
       g += nt;
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort) note_timeout(p.err, p.err_site, *abort);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// Joins the partial results of the units that range borders cut: block
-// (c, y) takes rows 32y.. of the unit that starts in CTA c's range.  A lane
-// is a row, a warp 8 channels: partials are stored channel group by channel
-// group with rows side by side, so both kernels access them coalesced.
+// Joins the partial results of the units that range borders cut.  A warp
+// takes 8 rows and 8 channels of a unit, its lanes the rows times four shares
+// of the partials (every fourth one), whose loads are then in flight at once;
+// the shares are added by shuffles.  Partials are stored channel group by
+// channel group with rows side by side, so both kernels access whole
+// sectors.  The last block to finish clears the counters.
+constexpr int kJoinRows = 8;
 template <int D, bool BF>
 __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_constant__ TreeParams p) {
   griddep_wait();
-  const Cut cut = p.cuts[blockIdx.x];
-  const int row = blockIdx.y * 32 + (threadIdx.x & 31), c8 = threadIdx.x >> 5;
-  if (row >= cut.rows) return;
-  const int X = row / kRows, r = row - X * kRows, rj = r / p.G, j = X * p.tile_tokens + rj;
-  if (rj >= p.tile_tokens || j >= cut.ntok) return;
-  const int t = cut.t0 + j, h = cut.k * p.G + (r - rj * p.G);
-  const int ns = cut.more + 1;
-  auto slot_of = [&](int s) -> size_t { return s == 0 ? cut.slot0 : 2 * (blockIdx.x + s); };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < ns; ++s) M = fmaxf(M, p.part_ml[slot_of(s) * p.part_rows + row].x);
-  float den = 0.f, acc[8] = {};
-#pragma unroll 4
-  for (int s = 0; s < ns; ++s) {
-    const size_t at = slot_of(s);
-    const float2 ml = p.part_ml[at * p.part_rows + row];
-    const float4* o = p.part_o + (at * (D / 4) + 2 * c8) * p.part_rows + row;
-    const float4 a = o[0], b = o[p.part_rows];
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    if (f != 0.f) {
-      den += f * ml.y;
-      acc[0] += f * a.x; acc[1] += f * a.y; acc[2] += f * a.z; acc[3] += f * a.w;
-      acc[4] += f * b.x; acc[5] += f * b.y; acc[6] += f * b.z; acc[7] += f * b.w;
+  const int lane = threadIdx.x & 31, c8 = threadIdx.x >> 5, share = lane >> 3;
+  const int row_groups = p.part_rows / kJoinRows, n_work = p.counters->n_cuts * row_groups;
+  for (int i = blockIdx.x; i < n_work; i += gridDim.x) {
+    const Cut cut = p.cuts[i / row_groups];
+    const int row = i % row_groups * kJoinRows + (lane & 7);
+    if (row - (lane & 7) >= cut.rows) continue;
+    const int ns = cut.more + 1;
+    auto slot_of = [&](int s) -> size_t { return s == 0 ? cut.slot0 : cut.slot1 + 2 * p.Hk * (s - 1); };
+    float m = -INFINITY, den = 0.f, acc[8] = {};
+#pragma unroll 2
+    for (int s = share; s < ns; s += 4) {
+      const size_t at = slot_of(s);
+      const float2 ml = p.part_ml[at * p.part_rows + row];
+      const float4* o = p.part_o + (at * (D / 4) + 2 * c8) * p.part_rows + row;
+      const float4 a = o[0], b = o[p.part_rows];
+      if (ml.x == -INFINITY) continue;
+      const float m_new = fmaxf(m, ml.x), f_old = ex2(m - m_new), f = ex2(ml.x - m_new);
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      den = m == -INFINITY ? ml.y * f : den * f_old + ml.y * f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = m == -INFINITY ? v[e] * f : acc[e] * f_old + v[e] * f;
+      m = m_new;
+    }
+    float M = m;
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+    const float f = m == -INFINITY ? 0.f : ex2(m - M);
+    den = f == 0.f ? 0.f : den * f;
+    den += __shfl_xor_sync(0xffffffffu, den, 8);
+    den += __shfl_xor_sync(0xffffffffu, den, 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      acc[e] = f == 0.f ? 0.f : acc[e] * f;
+      acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 8);
+      acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
+    }
+    const int X = row / kRows, r = row - X * kRows, rj = r / p.G, j = X * p.tile_tokens + rj;
+    if (share != 0 || row >= cut.rows || rj >= p.tile_tokens || j >= cut.ntok) continue;
+    const int t = cut.t0 + j, h = cut.k * p.G + (r - rj * p.G);
+    if (p.head_sink && M != -INFINITY) den += ex2(elem16_to_float(p.head_sink[h], BF) * kLog2e - M);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    *reinterpret_cast<uint4*>(p.out + ((size_t)t * p.H + h) * D + 8 * c8) =
+        make_uint4(pack2<BF>(acc[0] * inv, acc[1] * inv), pack2<BF>(acc[2] * inv, acc[3] * inv),
+                   pack2<BF>(acc[4] * inv, acc[5] * inv), pack2<BF>(acc[6] * inv, acc[7] * inv));
+  }
+  if (threadIdx.x == 0) {  // (n_cuts was read above)
+    __threadfence();
+    if (atomicAdd(&p.counters->joined, 1) == (int)gridDim.x - 1) {
+      p.counters->n_cuts = 0;
+      p.counters->joined = 0;
     }
   }
-  if (p.head_sink && M != -INFINITY) den += ex2(elem16_to_float(p.head_sink[h], BF) * kLog2e - M);
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  *reinterpret_cast<uint4*>(p.out + ((size_t)t * p.H + h) * D + 8 * c8) =
-      make_uint4(pack2<BF>(acc[0] * inv, acc[1] * inv), pack2<BF>(acc[2] * inv, acc[3] * inv),
-                 pack2<BF>(acc[4] * inv, acc[5] * inv), pack2<BF>(acc[6] * inv, acc[7] * inv));
 }
 
 template <int D, bool BF, bool GEN>
 cudaError_t configure() {
   using C = TreeCfg<D>;
   static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
-  static_assert(C::kSmemBytes <= kSmemLimit, "shared memory");
-  static_assert(C::kSlots >= 4, "K/V ring");
+  static_assert(C::smem_bytes(1) <= kSmemLimit && C::smem_bytes(2) <= kSmemLimit, "shared memory");
+  static_assert(C::slots(2) >= 4 && C::slots(1) <= kMaxSlots && kMaxSlots / 2 + 3 <= kMaskRing, "K/V ring");
   static_assert(2 * kKeys + 2 * D <= C::kTmemCols, "tensor memory");
-  return cudaFuncSetAttribute(tree_kernel<D, BF, GEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  return cudaFuncSetAttribute(tree_kernel<D, BF, GEN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              std::max(C::smem_bytes(1), C::smem_bytes(2)));
 }
 
 template <int D, bool BF>
@@ -891,12 +1016,11 @@ template <int D, bool BF>
 cudaError_t launch_db(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                       int grid, cudaStream_t s) {
   const bool gen = p.softcap > 0.f || p.slopes || p.window >= 1;
-  cudaError_t e = gen ? launch_pdl(tree_kernel<D, BF, true>, dim3(grid), kThreads, TreeCfg<D>::kSmemBytes, s, tq, tk,
-                                   tv, p)
-                      : launch_pdl(tree_kernel<D, BF, false>, dim3(grid), kThreads, TreeCfg<D>::kSmemBytes, s, tq, tk,
-                                   tv, p);
+  const int smem = TreeCfg<D>::smem_bytes(p.q_tiles);
+  cudaError_t e = gen ? launch_pdl(tree_kernel<D, BF, true>, dim3(grid), kThreads, smem, s, tq, tk, tv, p)
+                      : launch_pdl(tree_kernel<D, BF, false>, dim3(grid), kThreads, smem, s, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_join_kernel<D, BF>, dim3(grid, (p.part_rows + 31) / 32), D / 8 * 32, 0, s, p);
+  return launch_pdl(tree_join_kernel<D, BF>, dim3(4 * grid), D / 8 * 32, 0, s, p);
 }
 
 }  // namespace
