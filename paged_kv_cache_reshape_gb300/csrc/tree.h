@@ -105,7 +105,7 @@ struct TreeParams {
   Cut* cuts;                 // [chunks]
   float2* part_ml;           // [2 chunks][part_rows]
   float4* part_o;            // [2 chunks][D / 4][part_rows]
-  long long* groups;         // [CTAs][n_groups]: starts of the groups of 32 sequences (batches beyond one block)
+  int* groups;               // [CTAs][n_groups]: starts of the groups of 32 sequences (batches beyond one block)
   int n_groups;              // groups of this call
   int part_rows;
   int* err;

@@ -25,7 +25,7 @@ struct pa_tree_handle_s {
   int* err = nullptr;
   pa::TreeCounters* counters = nullptr;
   pa::Cut* cuts = nullptr;
-  long long* groups = nullptr;
+  int* groups = nullptr;
   float2* part_ml = nullptr;
   float4* part_o = nullptr;
   std::string msg = "no error";
@@ -308,7 +308,7 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   h->n_ranges = pick_ranges(h->num_sms, c.kv_num_heads);
   const size_t chunks = (size_t)h->n_ranges * c.kv_num_heads, D = c.head_size;
   const size_t o_cnt = 256, o_cut = 512, o_grp = o_cut + up(sizeof(pa::Cut) * chunks);
-  const size_t o_ml = o_grp + up(sizeof(long long) * h->num_sms * ((c.max_batch + 31) / 32));
+  const size_t o_ml = o_grp + up(sizeof(int) * h->num_sms * ((c.max_batch + 31) / 32));
   const size_t o_po = o_ml + up(sizeof(float2) * 2 * chunks * h->part_rows);
   const size_t ws_bytes = o_po + sizeof(float) * 2 * chunks * h->part_rows * D;
   if (e == cudaSuccess) e = cudaMalloc(&h->ws, ws_bytes);
@@ -323,7 +323,7 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   h->err = reinterpret_cast<int*>(w);
   h->counters = reinterpret_cast<pa::TreeCounters*>(w + o_cnt);
   h->cuts = reinterpret_cast<pa::Cut*>(w + o_cut);
-  h->groups = reinterpret_cast<long long*>(w + o_grp);
+  h->groups = reinterpret_cast<int*>(w + o_grp);
   h->part_ml = reinterpret_cast<float2*>(w + o_ml);
   h->part_o = reinterpret_cast<float4*>(w + o_po);
   *out = h;

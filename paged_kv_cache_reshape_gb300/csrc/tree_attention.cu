@@ -35,9 +35,9 @@
 // there and added to the rows that do admit them when O leaves tensor memory.
 //
 // Roles (384 threads): warpgroups 0 and 1, softmax and epilogue of the two
-// streams (thread = row = TMEM lane); warp 8 K/V producer (TMA, a ring of
-// slots in the order of their use), warp 9 TMEM owner and MMA issuer, warp
-// 10 takes chunks, publishes their segments and loads Q.
+// streams (thread = row = TMEM lane); warps 8 and 11 K and V producers (TMA,
+// one ring of slots in the order of their use), warp 9 TMEM owner and MMA
+// issuer, warp 10 takes chunks, publishes their segments and loads Q.
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -49,7 +49,8 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 12 * 32;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kFetchWarp = 10;
+constexpr int kKWarp = 8, kMmaWarp = 9, kFetchWarp = 10, kVWarp = 11;
+constexpr int kControlWarp0 = 8;
 // Registers per thread after the split (launch: 168 each).
 constexpr int kRegSoftmax = 208, kRegControl = 80;
 static_assert(2 * kRegSoftmax + kRegControl <= 3 * 168, "register split");
@@ -114,8 +115,8 @@ struct Ctrl {
   uint64_t info_full[kInfoRing], info_empty[kInfoRing];
   uint64_t xchg_full, xchg_done;
   uint64_t drain;
-  long long scan[kThreads / 32];      // lengths of the first groups of 32 sequences, then where they start
-  long long total;
+  int scan[kThreads / 32];            // lengths of the first groups of 32 sequences, then where they start
+  int total;                          // length of the line
   uint32_t tmem_base;
   int abort;
 };
@@ -138,7 +139,7 @@ struct SeqWork {
   int lo;        // first key walked (a multiple of 128)
   int nt;        // key tiles of each unit
   int pairs;     // units
-  long long len; // their length in the line
+  int len;       // their length in the line
 };
 
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bits) {
@@ -161,7 +162,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bit
     s.lo = p.window >= 1 ? (max(0, s.past + 1 - p.window) & ~(kKeys - 1)) : 0;
     s.nt = (s.past + s.n - s.lo + kKeys - 1) / kKeys;
     s.pairs = (s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-    s.len = (long long)(s.nt + kUnitCost) * s.pairs;
+    s.len = (s.nt + kUnitCost) * s.pairs;
   }
   return s;
 }
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kInfoRing; ++i) {
       mbar_init(&ctl->info_full[i], 1);
-      mbar_init(&ctl->info_empty[i], 1 + 8 + 1);  // MMA, softmax and K/V producer warps
+      mbar_init(&ctl->info_empty[i], 1 + 8 + 2);  // MMA, softmax and K/V producer warps
     }
     for (int i = 0; i < S; ++i) {
       mbar_init(&ctl->full[i], 1);
@@ -245,16 +246,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x < 4 * kTreeMaxWords) ctl->bad[0][0][threadIdx.x] = 0;
   if (warp == kFetchWarp && lane == 0) prefetch_tmap(&tm_q);
-  if (warp == kProducerWarp && lane == 0) {
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-  }
+  if (warp == kKWarp && lane == 0) prefetch_tmap(&tm_k);
+  if (warp == kVWarp && lane == 0) prefetch_tmap(&tm_v);
 
   griddep_wait();  // lengths, queries and pools may come from the previous kernel
   griddep_launch_dependents();
 
   // Where each group of 32 sequences starts in the line, and its length.
-  long long* const groups = p.batch <= kThreads ? ctl->scan : p.groups + (size_t)blockIdx.x * p.n_groups;
+  int* const groups = p.batch <= kThreads ? ctl->scan : p.groups + (size_t)blockIdx.x * p.n_groups;
   int bits = 0;
   long long before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
@@ -262,19 +261,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long len = b < p.batch ? seq_work(p, b, bits).len : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) len += __shfl_xor_sync(0xffffffffu, len, o);
+    // (no sum over a line of at most 2^31 - 1 wraps; a longer one is refused below)
     __syncthreads();
-    if (lane == 0) ctl->scan[warp] = len;
+    if (lane == 0) ctl->scan[warp] = (int)min(len, 0x7fffffffll);
     __syncthreads();
     long long first = before;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) first += ctl->scan[w];
       before += ctl->scan[w];
     }
     if (p.batch <= kThreads) __syncthreads();  // the groups' starts replace their lengths
-    if (lane == 0 && (b0 >> 5) + warp < p.n_groups) groups[(b0 >> 5) + warp] = first;
+    if (lane == 0 && (b0 >> 5) + warp < p.n_groups) groups[(b0 >> 5) + warp] = (int)first;
+  }
+  if (before > 0x7fffffffll) {  // 2^31 key tiles: days of work
+    bits |= PA_DEVERR_KV_BOUND;
+    before = 0;
   }
   if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
-  if (threadIdx.x == 0) ctl->total = before;
+  if (threadIdx.x == 0) ctl->total = (int)before;
   if ((smem_u32(smem) & 1023) != 0) {  // the swizzled operands need it; never seen
     if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
     return;
@@ -292,24 +297,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Register split: each warpgroup resizes at the top of its own branch
   // (the allocator budgets a branch from the setmaxnreg that dominates it).
-  if (warp >= kProducerWarp) {
+  if (warp >= kControlWarp0) {
     regs_dec<kRegControl>();
     if (warp == kFetchWarp) {
       // ---------------------------------------------------------- fetcher
       // Takes chunks, publishes their segments and loads a segment's Q tiles
       // once the previous segment's S products are done.
       const uint32_t q_bytes = C::kChunks * p.G * p.tile_tokens * 128;
-      const long long total = ctl->total;
-      const int n_ranges = (int)min((long long)p.n_ranges, (total + p.min_len - 1) / p.min_len);
-      const int n_chunks = n_ranges * p.Hk;
+      const int total = ctl->total;
+      const int n_ranges = min(p.n_ranges, total / p.min_len + 1);
+      const int n_chunks = total > 0 ? n_ranges * p.Hk : 0;
+      const int len_q = total / n_ranges, len_r = total - len_q * n_ranges;
+      auto range_begin = [&](int i) -> int { return len_q * i + min(i, len_r); };  // the first len_r are one longer
       // A window of 32 sequences, one per lane: where each ends in the line.
       int group = -1;
-      long long win_lo = 0, win_hi = 0, seq_end = 0;
+      int win_lo = 0, win_hi = 0, seq_end = 0;
       SeqWork mine{};
       int ignored = 0;
       uint32_t q_loads = 0;
       int chunk = (int)blockIdx.x - (int)gridDim.x, range = 0;
-      long long r = 0, r_begin = 0, r_end = 0;
+      int r = 0, r_begin = 0, r_end = 0;
       for (uint32_t tt = 0;; ++tt) {
         Segment f{};
         while (true) {
@@ -317,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             chunk += gridDim.x;
             if (chunk >= n_chunks) break;
             range = chunk / p.Hk;
-            r = r_begin = total * range / n_ranges;
-            r_end = total * (range + 1) / n_ranges;
+            r = r_begin = range_begin(range);
+            r_end = range_begin(range + 1);
             continue;
           }
           if (r >= win_hi || r < win_lo || group < 0) {
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             seq_end = mine.len;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-              const long long up = __shfl_up_sync(0xffffffffu, seq_end, o);
+              const int up = __shfl_up_sync(0xffffffffu, seq_end, o);
               if (lane >= o) seq_end += up;
             }
             seq_end += win_lo;
@@ -350,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           s.t0 = __shfl_sync(0xffffffffu, mine.t0, src);
           s.lo = __shfl_sync(0xffffffffu, mine.lo, src);
           s.nt = __shfl_sync(0xffffffffu, mine.nt, src);
-          const long long off = r - __shfl_sync(0xffffffffu, seq_end - mine.len, src);
-          const int u = (int)(off / (s.nt + kUnitCost)), tile0 = (int)(off - (long long)u * (s.nt + kUnitCost));
+          const int off = r - __shfl_sync(0xffffffffu, seq_end - mine.len, src);
+          const int u = off / (s.nt + kUnitCost), tile0 = off - u * (s.nt + kUnitCost);
           if (tile0 >= s.nt) {  // the unit's fixed cost
             r += s.nt + kUnitCost - tile0;
             continue;
@@ -366,15 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           f.n = s.n;
           f.past = s.past;
           f.key0 = s.lo + tile0 * kKeys;
-          f.nt = (int)min((long long)(s.nt - tile0), r_end - r);
+          f.nt = min(s.nt - tile0, r_end - r);
           f.slot = f.nt == s.nt ? -1 : 2 * chunk + (r == r_begin ? 0 : 1);
           if (tile0 == 0 && f.nt < s.nt && lane == 0) {  // the unit goes on in later ranges
             Cut cut{};
             cut.rows = f.two ? kRows + (f.ntok - p.tile_tokens) * p.G : f.ntok * p.G;
             cut.slot0 = f.slot;
             cut.slot1 = 2 * (chunk + p.Hk);
-            // the range that holds the unit's last tile: the largest i with total * i / n_ranges <= last
-            cut.more = (int)(((r + s.nt) * n_ranges - 1) / total) - range;
+            cut.more = 0;
+            while (range_begin(range + cut.more + 1) < r + s.nt) ++cut.more;
             cut.t0 = f.t0;
             cut.ntok = f.ntok;
             cut.k = f.k;
@@ -413,16 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&ctl->q_full, (q_loads - 1) & 1); ++i) {
         }
       }
-    } else if (warp == kProducerWarp) {
-      // ----------------------------------------------------- K/V producer
-      uint32_t n_loads = 0, n_tiles = 0;  // K/V slot loads and key tiles issued so far
+    } else if (warp == kKWarp || warp == kVWarp) {
+      // ---------------------------------------------------- K, V producers
+      // Both walk the same loads (in the order of use, see the MMA issuer:
+      // K_i V_i with two row tiles, K_i V_{i-1} with one) and issue their own.
+      const bool v_warp = warp == kVWarp;
+      const CUtensorMap* tm = v_warp ? &tm_v : &tm_k;
+      uint32_t n_tiles = 0;             // tiles issued so far
+      uint32_t issued = 0, phases = 0;  // per slot: loaded by this warp; the phase of that load
       RingPos at;
       bool ok = true;
       for (uint32_t tt = 0; ok; ++tt) {
         const int slot = tt % kInfoRing;
         int got = 1;
-        if (lane == 0)
-          got = tree_wait(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, 4);
+        if (lane == 0) got = tree_wait(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, 4);
         if (!__shfl_sync(0xffffffffu, got, 0)) break;
         const Segment cur = ctl->seg[slot];
         if (!cur.live) break;
@@ -431,22 +442,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load_id = [&](int e) -> int {
           return (e < p.MB && ((long long)e << p.log_bs) < end) ? bt_row[e] : -1;
         };
+        // block ids of 32 pages, one per lane, and of the 32 behind them
         int win = cur.key0 >> p.log_bs;
-        int id = load_id(win + lane), rc = p.oob_row, rc_before = 0;
-        // In the order of use (see the MMA issuer): K_i V_i with two row
-        // tiles, K_i V_{i-1} with one.
+        int id = load_id(win + lane), id_next = load_id(win + 32 + lane), rc = p.oob_row, rc_before = 0;
         const int lag = cur.two ? 0 : 1;
 #pragma unroll 1
-        for (int l = 0; l < 2 * (cur.nt + lag) && ok; ++l) {
+        for (int l = 0; l < 2 * (cur.nt + lag); ++l) {
           const bool is_v = l & 1;
           const int i = l >> 1;
-          uint32_t mask = 0;
           if (is_v ? i < lag : i >= cur.nt) continue;
+          uint32_t mask = 0;
           if (!is_v) {  // the tile's pages
             const int key0 = cur.key0 + i * kKeys;
             if (((key0 + kKeys - 1) >> p.log_bs) >= win + 32) {
-              win = key0 >> p.log_bs;
-              id = load_id(win + lane);
+              win += 32;
+              id = id_next;
+              id_next = load_id(win + 32 + lane);
             }
             const int pos = key0 + (lane << log_r);
             const int idx = (pos >> p.log_bs) - win;
@@ -459,37 +470,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mask = __ballot_sync(0xffffffffu, lane < pages && rc == p.oob_row);
           }
-          // Into the next ring slot: lane l copies page l.
-          if (lane == 0) {
-            if (!tree_wait(&ctl->empty[at.slot], at.phase ^ 1, abort, 3)) {
-              ok = false;
-            } else {
-              if (!is_v) {
-                ctl->kv_mask[n_tiles % kMaskRing] = (uint8_t)mask;
-                mbar_arrive(&ctl->mask_full[n_tiles % kMaskRing]);
+          if (is_v == v_warp) {  // into the ring's next slot: lane l copies page l
+            if (lane == 0) {
+              if (!tree_wait(&ctl->empty[at.slot], at.phase ^ 1, abort, 3)) {
+                ok = false;
+              } else {
+                if (!is_v) {
+                  ctl->kv_mask[n_tiles % kMaskRing] = (uint8_t)mask;
+                  mbar_arrive(&ctl->mask_full[n_tiles % kMaskRing]);
+                }
+                mbar_arrive_expect_tx(&ctl->full[at.slot], C::kSlotBytes);
               }
-              mbar_arrive_expect_tx(&ctl->full[at.slot], C::kSlotBytes);
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const int row = is_v && lag && i < cur.nt ? rc_before : rc;
+            if (lane < pages)
+              tma_load_5d(kv_s + at.slot * C::kSlotBytes + (lane << (log_r - 3)) * C::kGroupBytes, tm, 0, 0, 0, row >> 3,
+                          cur.k, &ctl->full[at.slot]);
+            issued |= 1u << at.slot;
+            phases = (phases & ~(1u << at.slot)) | (at.phase << at.slot);
+            ++n_tiles;
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          const int row = is_v && lag && i < cur.nt ? rc_before : rc;
-          if (lane < pages)
-            tma_load_5d(kv_s + at.slot * C::kSlotBytes + (lane << (log_r - 3)) * C::kGroupBytes, is_v ? &tm_v : &tm_k, 0,
-                        0, 0, row >> 3, cur.k, &ctl->full[at.slot]);
-          ++n_loads;
-          n_tiles += is_v ? 0 : 1;
           at.next(S);
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(&ctl->info_empty[slot]);
       }
       if (lane == 0 && *abort) {
-        for (int d = 1; d <= S && (int)n_loads - d >= 0; ++d) {
-          const uint32_t n = n_loads - d;
-          for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&ctl->full[n % S], (n / S) & 1); ++i) {
+        // Gave up: let the copies already issued land before the CTA exits.
+        for (int i = 0; i < S; ++i)
+          for (uint32_t k = 0; ((issued >> i) & 1) && k < kWaitLimit && !mbar_try_wait(&ctl->full[i], (phases >> i) & 1); ++k) {
           }
-        }
       }
     } else if (warp == kMmaWarp) {
       // -------------------------------------------------------- MMA issuer
@@ -940,11 +952,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinRows = 8;
 template <int D, bool BF>
 __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  griddep_wait();
   const int lane = threadIdx.x & 31, c8 = threadIdx.x >> 5, share = lane >> 3;
-  const int row_groups = p.part_rows / kJoinRows, n_work = p.counters->n_cuts * row_groups;
+  const int row_groups = p.part_rows / kJoinRows;
+  griddep_wait();
+  griddep_launch_dependents();
+  // the first cut is read beside the count (entries behind it are stale, not used)
+  Cut cut = p.cuts[min((int)blockIdx.x / row_groups, p.n_ranges * p.Hk - 1)];
+  const int n_work = p.counters->n_cuts * row_groups;
   for (int i = blockIdx.x; i < n_work; i += gridDim.x) {
-    const Cut cut = p.cuts[i / row_groups];
+    if (i != (int)blockIdx.x) cut = p.cuts[i / row_groups];
     const int row = i % row_groups * kJoinRows + (lane & 7);
     if (row - (lane & 7) >= cut.rows) continue;
     const int ns = cut.more + 1;
