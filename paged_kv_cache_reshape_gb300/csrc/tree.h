@@ -93,12 +93,13 @@ struct TreeParams {
   __half* out;
   int batch, T;
   int H, Hk, G, D;
-  int tile_tokens;           // tokens of a 128-row tile
+  int tile_tokens;           // tokens of a row tile (128 / rep rows)
   int bs, NB, MB, log_bs, log_page_rows, oob_row;
   int max_draft, words, max_kv;
   int window;
-  int n_ranges, min_len;     // ranges of the line; the smallest, in tiles
+  int n_ranges;              // ranges of the line at most
   int q_tiles;               // 2 when a unit may have two row tiles
+  int rep;                   // replicas of the rows (1, 2 or 4)
   float scale, softcap;
   // workspace
   TreeCounters* counters;
@@ -111,8 +112,16 @@ struct TreeParams {
   int* err;
   int* err_site;
 };
-cudaError_t tree_configure(int head_size, int bf16);
+template <int D>
+cudaError_t tree_configure(int bf16, int rep);
+template <int D>
 cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                         int bf16, int grid, cudaStream_t s);
+template <> cudaError_t tree_configure<64>(int, int);
+template <> cudaError_t tree_configure<128>(int, int);
+template <> cudaError_t launch_tree<64>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const TreeParams&,
+                                        int, int, cudaStream_t);
+template <> cudaError_t launch_tree<128>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const TreeParams&,
+                                         int, int, cudaStream_t);
 
 }  // namespace pa

@@ -20,7 +20,7 @@ struct pa_tree_handle_s {
   int max_draft = 0, words = 0, max_kv = 0;
   float scale = 0.f;
   bool bf16 = false;
-  int tile_tokens = 1, part_rows = 0, n_ranges = 1;
+  int tile_tokens = 1, part_rows = 0, n_ranges = 1, rep = 1;
   void* ws = nullptr;
   int* err = nullptr;
   pa::TreeCounters* counters = nullptr;
@@ -297,12 +297,18 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   h->max_kv = c.max_kv_len_bound > 0 ? std::min(c.max_kv_len_bound, kv_cap) : kv_cap;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
-  if (e == cudaSuccess) e = pa::tree_configure(c.head_size, h->bf16);
   // Workspace: error word, counters, the cut units, the starts of the groups
   // of sequences (per CTA) and two partial results per chunk (256-byte
   // aligned pieces).
   const int G = c.num_heads / c.kv_num_heads;
-  h->tile_tokens = pa::kPrefillRows / G;
+  // Replicas of the rows where few rows would leave most softmax warps idle.
+  // At head_size 128 the K/V stream covers one warp's softmax, and there is
+  // no shared memory left to join replicas in.
+  const int rows = max_draft_tokens * G;
+  h->rep = c.head_size == 64 ? (rows <= 32 ? 4 : rows <= 64 ? 2 : 1) : 1;
+  h->tile_tokens = pa::kPrefillRows / h->rep / G;
+  if (e == cudaSuccess)
+    e = c.head_size == 64 ? pa::tree_configure<64>(h->bf16, h->rep) : pa::tree_configure<128>(h->bf16, h->rep);
   h->part_rows = max_draft_tokens > h->tile_tokens ? 2 * pa::kPrefillRows : (max_draft_tokens * G + 31) / 32 * 32;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   h->n_ranges = pick_ranges(h->num_sms, c.kv_num_heads);
@@ -467,7 +473,7 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   while ((1 << p.log_page_rows) < page_rows) ++p.log_page_rows;
   p.oob_row = c.num_blocks * c.block_size;
   p.n_ranges = h->n_ranges;
-  p.min_len = 1;
+  p.rep = h->rep;
   p.q_tiles = h->max_draft > h->tile_tokens ? 2 : 1;
   p.counters = h->counters;
   p.groups = h->groups;
@@ -483,7 +489,9 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
       !pa::encode_groups_map(&tk, key_cache, D, Hk, (long long)c.num_blocks * c.block_size, page_rows) ||
       !pa::encode_groups_map(&tv, value_cache, D, Hk, (long long)c.num_blocks * c.block_size, page_rows))
     return tree_fail(h, PA_CUDA_ERROR, "cuTensorMapEncodeTiled failed");
-  cudaError_t e = pa::launch_tree(tq, tk, tv, p, h->bf16, h->num_sms, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = D == 64 ? pa::launch_tree<64>(tq, tk, tv, p, h->bf16, h->num_sms, s)
+                          : pa::launch_tree<128>(tq, tk, tv, p, h->bf16, h->num_sms, s);
   if (e != cudaSuccess) return tree_cuda_fail(h, e, "tree attention launch");
   return PA_OK;
 }

@@ -27,6 +27,12 @@
 // N 128 columns, O = head_size columns), P over S as 16-bit pairs, read from
 // there by the P V product.
 //
+// Few rows (head_size 64, at most 64 or 32): the row tile holds every row 2 or
+// 4 times (REP), each replica takes the softmax of its own half or quarter of
+// a tile's keys (its P is zero at the others), and the replicas' O, m and l
+// are joined in shared memory at the segment's end: otherwise one or two
+// warps of four would do all the exponentials.
+//
 // Masks: an interior tile (context only) needs none.  A tile that holds
 // draft tokens, a window's edge or an unmapped page builds one 128-bit mask
 // per row.  P is zero at masked keys, and 0 * inf would still be NaN in the
@@ -66,6 +72,7 @@ constexpr int kInfoRing = 4;  // segments published ahead of their use
 // of all older tiles but the last few).
 constexpr int kMaskRing = 16;
 constexpr int kMaxSlots = 12;  // K/V ring slots at most
+constexpr int kJoinChannels = 16;  // channels of the replicas joined at a time
 constexpr int kUnitCost = 2;  // a unit's fixed cost in key tiles
 
 template <int D>
@@ -75,15 +82,19 @@ struct TreeCfg {
   static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V tile [key / 8][chunk][key % 8][128 B]
   static constexpr int kGroupBytes = kChunks * 1024;  // its 8-key groups
   // Slots of the K/V ring beside `q_tiles` Q tiles.
-  static __host__ __device__ constexpr int slots(int q_tiles) {
-    const int fit = (kSmemLimit - kCtrlBytes - q_tiles * kQTileBytes) / kSlotBytes;
+  static __host__ __device__ constexpr int slots(int q_tiles, int rep) {
+    const int fit = (kSmemLimit - kCtrlBytes - join_bytes(rep) - q_tiles * kQTileBytes) / kSlotBytes;
     return fit < kMaxSlots ? fit : kMaxSlots;
+  }
+  // Where replicas are joined: per stream 128 lanes x 16 channels, and (m, l) per row.
+  static __host__ __device__ constexpr int join_bytes(int rep) {
+    return rep > 1 ? 2 * kRows * kJoinChannels * 4 + 2 * kRows * 8 : 0;
   }
   static __host__ __device__ constexpr int s_col(int X) { return X * kKeys; }
   static __host__ __device__ constexpr int o_col(int X) { return 2 * kKeys + X * D; }
   static constexpr int kTmemCols = 512;
-  static __host__ __device__ constexpr int smem_bytes(int q_tiles) {
-    return q_tiles * kQTileBytes + slots(q_tiles) * kSlotBytes + kCtrlBytes;
+  static __host__ __device__ constexpr int smem_bytes(int q_tiles, int rep) {
+    return q_tiles * kQTileBytes + slots(q_tiles, rep) * kSlotBytes + kCtrlBytes + join_bytes(rep);
   }
 };
 
@@ -113,7 +124,7 @@ struct Ctrl {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t info_full[kInfoRing], info_empty[kInfoRing];
-  uint64_t xchg_full, xchg_done;
+  uint64_t xchg_full, xchg_done, join[2];
   uint64_t drain;
   int scan[kThreads / 32];            // lengths of the first groups of 32 sequences, then where they start
   int total;                          // length of the line
@@ -206,13 +217,14 @@ __device__ __forceinline__ uint32_t bad_word(const Ctrl* ctl, int parity, int i)
 }
 
 // GEN: softcap, distance bias or a window (checked at run time); without it
-// the scores need one multiplication.
-template <int D, bool BF, bool GEN>
+// the scores need one multiplication.  REP: replicas of the rows.
+template <int D, bool BF, bool GEN, int REP>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D>;
-  const int S = C::slots(p.q_tiles);
+  static_assert(REP == 1 || D == 64, "replicated rows");
+  const int S = C::slots(p.q_tiles, REP);
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* q_s = smem;                                // [tile A (, tile B)]
   uint8_t* kv_s = q_s + p.q_tiles * C::kQTileBytes;  // [slot]
@@ -240,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMaskRing; ++i) mbar_init(&ctl->mask_full[i], 1);
     mbar_init(&ctl->xchg_full, 8);
     mbar_init(&ctl->xchg_done, 8);
+    mbar_init(&ctl->join[0], 4);
+    mbar_init(&ctl->join[1], 4);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -303,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- fetcher
       // Takes chunks, publishes their segments and loads a segment's Q tiles
       // once the previous segment's S products are done.
-      const uint32_t q_bytes = C::kChunks * p.G * p.tile_tokens * 128;
+      const uint32_t q_bytes = C::kChunks * p.G * p.tile_tokens * 128;  // of one box
       const int total = ctl->total;
-      const int n_ranges = min(p.n_ranges, total / p.min_len + 1);
+      const int n_ranges = min(p.n_ranges, total + 1);
       const int n_chunks = total > 0 ? n_ranges * p.Hk : 0;
       const int len_q = total / n_ranges, len_r = total - len_q * n_ranges;
       auto range_begin = [&](int i) -> int { return len_q * i + min(i, len_r); };  // the first len_r are one longer
@@ -319,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int r = 0, r_begin = 0, r_end = 0;
       for (uint32_t tt = 0;; ++tt) {
         Segment f{};
+        Cut cut{};
         while (true) {
           if (r >= r_end) {  // next chunk
             chunk += gridDim.x;
@@ -375,8 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f.key0 = s.lo + tile0 * kKeys;
           f.nt = min(s.nt - tile0, r_end - r);
           f.slot = f.nt == s.nt ? -1 : 2 * chunk + (r == r_begin ? 0 : 1);
-          if (tile0 == 0 && f.nt < s.nt && lane == 0) {  // the unit goes on in later ranges
-            Cut cut{};
+          if (tile0 == 0 && f.nt < s.nt) {  // the unit goes on in later ranges
             cut.rows = f.two ? kRows + (f.ntok - p.tile_tokens) * p.G : f.ntok * p.G;
             cut.slot0 = f.slot;
             cut.slot1 = 2 * (chunk + p.Hk);
@@ -385,7 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             cut.t0 = f.t0;
             cut.ntok = f.ntok;
             cut.k = f.k;
-            p.cuts[atomicAdd(&p.counters->n_cuts, 1)] = cut;
           }
           r += f.nt;
           break;
@@ -402,16 +415,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!tree_wait(&ctl->q_empty, (tt & 1) ^ 1, abort, 2)) {
                 ok = false;
               } else {
-                mbar_arrive_expect_tx(&ctl->q_full, (f.two ? 2 : 1) * q_bytes);
-                for (int X = 0; X < (f.two ? 2 : 1); ++X)
+                // both row tiles, or the one, or its replicas
+                const int boxes = f.two ? 2 : REP;
+                mbar_arrive_expect_tx(&ctl->q_full, boxes * q_bytes);
+#pragma unroll 1
+                for (int i = 0; i < boxes; ++i)
                   for (int c = 0; c < C::kChunks; ++c)
-                    tma_load_3d(q_s + X * C::kQTileBytes + c * (kRows * 128), &tm_q, c * 64, f.k * p.G,
-                                f.t0 + X * p.tile_tokens, &ctl->q_full);
+                    tma_load_3d(q_s + i * (f.two ? C::kQTileBytes : kRows / REP * 128) + c * (kRows * 128), &tm_q, c * 64,
+                                f.k * p.G, f.t0 + (f.two ? i * p.tile_tokens : 0), &ctl->q_full);
                 ++q_loads;
               }
             }
           }
         }
+        if (lane == 0 && cut.rows > 0) p.cuts[atomicAdd(&p.counters->n_cuts, 1)] = cut;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok || !f.live) break;
       }
@@ -589,13 +606,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_inc<kRegSoftmax>();
     // ------------------------------------------- softmax and epilogue warps
     const int X = warp >> 2;            // stream
-    const int r = threadIdx.x & 127;    // row of the tile == TMEM lane
-    const int rj = r / p.G;             // its token within the tile
+    constexpr int R = kRows / REP, COLS = kKeys / REP;
+    const int r = threadIdx.x & 127;    // TMEM lane
+    const int row = r & (R - 1);        // row of the tile
+    const int cb = r / R * COLS;        // first of the tile's keys that this replica takes
+    const int rj = row / p.G;           // the row's token within the tile
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float mul = GEN && (p.softcap > 0.f || p.slopes) ? 1.f : p.scale * kLog2e;
     uint32_t g = 0, scnt = 0, ocnt[2] = {0, 0};
     RingPos ring;  // of the segment's first load
-    float x[kKeys];
+    float x[COLS < 64 ? 64 : COLS];
+    uint32_t joins = 0;  // phase of join[X]
     for (uint32_t tt = 0;; ++tt) {
       const int slot = tt % kInfoRing;
       if (!tree_wait(&ctl->info_full[slot], (tt / kInfoRing) & 1, abort, 6)) break;
@@ -617,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (GEN) {
         qpos = p.positions ? p.positions[t] : past + j_seq;
         if (p.window >= 1) lo_row = max(max(qpos, past) - p.window + 1, 0);
-        if (p.slopes && row_ok) slope2 = p.slopes[sg.k * p.G + (r - rj * p.G)] * kLog2e;
+        if (p.slopes && row_ok) slope2 = p.slopes[sg.k * p.G + (row - rj * p.G)] * kLog2e;
       }
       const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;  // no row admits a key below
       if (p.mask && row_ok && sg.key0 + nt * kKeys > past) {
@@ -642,35 +663,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (made before the wait for S).
         const bool partial = key0 + kKeys > past || pmask != 0 || __any_sync(0xffffffffu, key0 < lo_row || !row_ok);
         const bool drafts = key0 + kKeys > past;
-        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-        float kpf[4];  // GEN: lane e, entry q: position of key 32 q + e, less past
-        if constexpr (GEN) {
+        constexpr int NW = COLS / 32;
+        uint32_t w[NW];
+        float kpf[NW];  // GEN: lane e, entry q: position of key cb + 32 q + e, less past
 #pragma unroll
-          for (int q = 0; q < 4; ++q) kpf[q] = (float)(key0 + 32 * q + lane - past);
+        for (int q = 0; q < NW; ++q) {
+          w[q] = ~0u;
+          if constexpr (GEN) kpf[q] = (float)(key0 + cb + 32 * q + lane - past);
         }
         if (partial && warp_ok) {
-          int kp[4];
+          int kp[NW];
           if constexpr (GEN) {
             if (drafts && p.positions) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int d = key0 + 32 * q + lane - past;
+              for (int q = 0; q < NW; ++q) {
+                const int d = key0 + cb + 32 * q + lane - past;
                 kp[q] = d >= 0 && d < n ? p.positions[sg.seq_t0 + d] : past + d;
                 kpf[q] = (float)(kp[q] - past);
               }
             }
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int k0 = key0 + 32 * q, d0 = k0 - past;  // d0: draft index of bit 0
+          for (int q = 0; q < NW; ++q) {
+            const int k0 = key0 + cb + 32 * q, d0 = k0 - past;  // d0: draft index of bit 0
             uint32_t m = bit_range(lo_row - k0, -d0);
             if (d0 + 32 > 0 && d0 < n) {
               uint32_t md = bit_range(-d0, n - d0);
               if (p.mask) {
-                const uint32_t* row = p.mask + (size_t)t * p.words;
+                const uint32_t* mrow = p.mask + (size_t)t * p.words;
                 const int wi = d0 >> 5;  // (floor)
-                const uint32_t a = wi >= 0 ? row[wi] : 0u;
-                const uint32_t b = wi + 1 < p.words ? row[wi + 1] : 0u;
+                const uint32_t a = wi >= 0 ? mrow[wi] : 0u;
+                const uint32_t b = wi + 1 < p.words ? mrow[wi + 1] : 0u;
                 md &= __funnelshift_r(a, b, d0 & 31);
               } else {
                 md &= bit_range(0, j_seq + 1 - d0);
@@ -696,7 +719,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g2 = 0; g2 < pages; ++g2) {
               if (!((pmask >> g2) & 1)) continue;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) w[q] &= ~bit_range((g2 << log_r) - 32 * q, ((g2 + 1) << log_r) - 32 * q);
+              for (int q = 0; q < NW; ++q)
+                w[q] &= ~bit_range((g2 << log_r) - cb - 32 * q, ((g2 + 1) << log_r) - cb - 32 * q);
             }
           }
         }
@@ -709,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (warp_ok) {
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) tmem_ld32(lane_addr + C::s_col(X) + c, x + c);
+          for (int c = 0; c < COLS; c += 32) tmem_ld32(lane_addr + C::s_col(X) + cb + c, x + c);
           tmem_ld_wait();
           if constexpr (GEN) {
             if (p.softcap > 0.f) {
@@ -717,20 +741,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               // approximate reciprocal is off by 2^-23 of a term below 2 c)
               const float in = 2.f * kLog2e * p.scale / p.softcap, out = p.softcap * kLog2e;
 #pragma unroll
-              for (int c = 0; c < kKeys; ++c) x[c] = fmaf(-2.f * out, rcp(1.f + ex2(x[c] * in)), out);
+              for (int c = 0; c < COLS; ++c) x[c] = fmaf(-2.f * out, rcp(1.f + ex2(x[c] * in)), out);
             }
             if (p.slopes) {
               const float unit = p.softcap > 0.f ? 1.f : p.scale * kLog2e, base = slope2 * (float)(past - qpos);
 #pragma unroll
-              for (int c = 0; c < kKeys; ++c)
+              for (int c = 0; c < COLS; ++c)
                 x[c] = fmaf(x[c], unit, fmaf(slope2, __shfl_sync(0xffffffffu, kpf[c >> 5], c & 31), base));
             }
           }
           if (partial) {
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c) x[c] = ((w[c >> 5] >> (c & 31)) & 1) ? x[c] : -INFINITY;
+            for (int c = 0; c < COLS; ++c) x[c] = ((w[c >> 5] >> (c & 31)) & 1) ? x[c] : -INFINITY;
           }
-          const float cand = max_tree<kKeys>(x) * mul;
+          const float cand = max_tree<COLS>(x) * mul;
           float alpha = 1.f;
           if (cand > m_ref + kLazyRescale || (m_ref == -INFINITY && cand != -INFINITY)) {
             alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - cand);
@@ -740,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t mul2 = f2(mul, mul), neg_m2 = f2(-m_use, -m_use);
           uint64_t sum2[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int h = 0; h < kKeys; h += 32) {
+          for (int h = 0; h < COLS; h += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
@@ -752,7 +776,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[q] = pack2<BF>(e0, e1);
             }
             // P -> TMEM over S: keys h..h+31 as 16 columns of 16-bit pairs
-            tmem_st16(lane_addr + C::s_col(X) + h / 2, pk);
+            tmem_st16(lane_addr + C::s_col(X) + (cb + h) / 2, pk);
+          }
+          if constexpr (REP > 1) {  // ... and zeros at the other replicas' keys
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int h = 0; h < kKeys; h += 32)
+              if (h < cb || h >= cb + COLS) tmem_st16(lane_addr + C::s_col(X) + h / 2, zero);
           }
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
             float o[32];
@@ -833,11 +863,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!tree_wait(&ctl->xchg_full, tt & 1, abort, 11)) break;
       float f0 = 1.f, f1 = 1.f;  // factors of O_0 and O_1 (one row tile)
       if (!two) {
-        const float2 a = ctl->ml[0][r], b = ctl->ml[1][r];
-        m_ref = fmaxf(a.x, b.x);
-        f0 = a.x == -INFINITY ? 0.f : ex2(a.x - m_ref);
-        f1 = b.x == -INFINITY ? 0.f : ex2(b.x - m_ref);
-        l = (f0 == 0.f ? 0.f : f0 * a.y) + (f1 == 0.f ? 0.f : f1 * b.y);
+        // over both streams and all replicas of the row
+        float2 ml[2 * REP];
+        m_ref = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * REP; ++i) {
+          ml[i] = ctl->ml[i & 1][(i >> 1) * R + row];
+          m_ref = fmaxf(m_ref, ml[i].x);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * REP; ++i) {
+          const float f = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - m_ref);
+          if (f != 0.f) l += f * ml[i].y;
+          if ((i >> 1) == (REP > 1 ? r / R : 0)) {
+            if (i & 1) f1 = f;
+            else f0 = f;
+          }
+        }
       }
       uint32_t any_bad = lane < kTreeMaxWords ? bad_word(ctl, tt & 1, 32 * lane) : 0u;
       any_bad = __any_sync(0xffffffffu, any_bad != 0);
@@ -854,20 +897,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      const int h = sg.k * p.G + (r - rj * p.G);
+      const int h = sg.k * p.G + (row - rj * p.G);
       float inv = 1.f;
       if (sg.slot < 0) {
         if (p.head_sink && row_ok && m_ref != -INFINITY)
           l += ex2(elem16_to_float(p.head_sink[h], BF) * kLog2e - m_ref);
         inv = l == 0.f ? 0.f : 1.f / l;
       }
-      const int row = (two ? X * kRows : 0) + r;  // row of the unit's partial result
-      if (sg.slot >= 0 && row_ok && (two || X == 0)) p.part_ml[(size_t)sg.slot * p.part_rows + row] = make_float2(m_ref, l);
+      const int urow = (two ? X * kRows : 0) + row;  // row of the unit's partial result
+      if (sg.slot >= 0 && row_ok && (two || threadIdx.x < R))
+        p.part_ml[(size_t)sg.slot * p.part_rows + urow] = make_float2(m_ref, l);
       __half* dst = p.out + ((size_t)t * p.H + h) * D;
-      float4* part = sg.slot >= 0 ? p.part_o + (size_t)sg.slot * (D / 4) * p.part_rows + row : nullptr;
+      float4* part = sg.slot >= 0 ? p.part_o + (size_t)sg.slot * (D / 4) * p.part_rows + urow : nullptr;
       // Two row tiles: every channel of the own O; one: half the channels of both.
       const int c0 = two ? 0 : X * (D / 2), c1 = two ? D : c0 + D / 2;
-      if (warp_ok) {
+      if constexpr (REP > 1) {
+        // The replicas' O, scaled, side by side in shared memory, 16 channels
+        // of this stream's half at a time; then each thread adds up four
+        // channels of a row in replica order and stores them.
+        float4* red = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(ctl) + kCtrlBytes) + X * kRows * kJoinChannels / 4;
+        float2* stat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ctl) + kCtrlBytes + 2 * kRows * kJoinChannels * 4) +
+                       X * kRows;
+        auto join_all = [&]() -> bool {  // the four warps of this stream
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->join[X]);
+          return tree_wait(&ctl->join[X], joins++ & 1, abort, 14);
+        };
+        if (r < R) stat[row] = make_float2(__int_as_float(row_ok ? t * p.H + h : -1), inv);
+#pragma unroll 1
+        for (int c = c0; c < c1 && ok; c += kJoinChannels) {
+          if (warp_ok) {
+            tmem_ld16(lane_addr + C::o_col(0) + c, x);
+            if (have[1]) tmem_ld16(lane_addr + C::o_col(1) + c, x + 16);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              x[e] = f0 == 0.f ? 0.f : x[e] * f0;
+              if (f1 != 0.f) x[e] = fmaf(x[16 + e], f1, x[e]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)  // (the exchange of vectors spreads a warp's stores over the banks)
+              red[r * 4 + (q ^ ((r >> 1) & 3))] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          }
+          ok = join_all();
+#pragma unroll
+          for (int i = 0; i < R * 4 / kRows && ok; ++i) {
+            const int item = i * kRows + r, orow = item >> 2, q = item & 3;
+            const float2 st = stat[orow];
+            const int at = __float_as_int(st.x);  // (token, head) of the row, -1: none
+            if (at < 0) continue;
+            float4 v = red[orow * 4 + (q ^ ((orow >> 1) & 3))];
+#pragma unroll
+            for (int k = 1; k < REP; ++k) {
+              const float4 u = red[(k * R + orow) * 4 + (q ^ ((orow >> 1) & 3))];
+              v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+            }
+            if (sg.slot >= 0)
+              p.part_o[((size_t)sg.slot * (D / 4) + c / 4 + q) * p.part_rows + orow] = v;
+            else
+              *reinterpret_cast<uint2*>(p.out + (size_t)at * D + c + 4 * q) =
+                  make_uint2(pack2<BF>(v.x * st.y, v.y * st.y), pack2<BF>(v.z * st.y, v.w * st.y));
+          }
+          ok = ok && join_all();
+        }
+        if (!ok) break;
+      } else if (warp_ok) {
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           tmem_ld32(lane_addr + C::o_col(0) + (two ? X * D : 0) + c, x);
@@ -903,9 +997,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&ctl->o_free[0]);
         mbar_arrive(&ctl->o_free[1]);
       }
-      if (any_bad && row_ok) {
+      if (any_bad && row_ok && r < R) {
         // Draft keys with non-finite V: added, element by element, to what
-        // this thread has just stored for its row if the row admits them.
+        // has just been stored for the row if the row admits them.
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
           if (!((bad_word(ctl, tt & 1, i) >> (i & 31)) & 1) || !mask_bit(p, t, j_seq, i)) continue;
@@ -1011,45 +1105,66 @@ __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_cons
   }
 }
 
-template <int D, bool BF, bool GEN>
+template <int D, bool BF, bool GEN, int REP>
 cudaError_t configure() {
   using C = TreeCfg<D>;
   static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
-  static_assert(C::smem_bytes(1) <= kSmemLimit && C::smem_bytes(2) <= kSmemLimit, "shared memory");
-  static_assert(C::slots(2) >= 4 && C::slots(1) <= kMaxSlots && kMaxSlots / 2 + 3 <= kMaskRing, "K/V ring");
+  constexpr int kQTiles = REP > 1 ? 1 : 2;
+  static_assert(C::smem_bytes(1, REP) <= kSmemLimit && C::smem_bytes(kQTiles, REP) <= kSmemLimit, "shared memory");
+  static_assert(C::slots(kQTiles, REP) >= 4 && kMaxSlots / 2 + 3 <= kMaskRing, "K/V ring");
   static_assert(2 * kKeys + 2 * D <= C::kTmemCols, "tensor memory");
-  return cudaFuncSetAttribute(tree_kernel<D, BF, GEN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              std::max(C::smem_bytes(1), C::smem_bytes(2)));
+  return cudaFuncSetAttribute(tree_kernel<D, BF, GEN, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              std::max(C::smem_bytes(1, REP), C::smem_bytes(kQTiles, REP)));
 }
 
-template <int D, bool BF>
-cudaError_t configure_db() {
-  const cudaError_t e = configure<D, BF, false>();
-  return e != cudaSuccess ? e : configure<D, BF, true>();
+template <int D, bool BF, int REP>
+cudaError_t configure_dbr() {
+  const cudaError_t e = configure<D, BF, false, REP>();
+  return e != cudaSuccess ? e : configure<D, BF, true, REP>();
 }
 
-template <int D, bool BF>
-cudaError_t launch_db(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
-                      int grid, cudaStream_t s) {
+template <int D, bool BF, int REP>
+cudaError_t launch_dbr(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                       int grid, cudaStream_t s) {
   const bool gen = p.softcap > 0.f || p.slopes || p.window >= 1;
-  const int smem = TreeCfg<D>::smem_bytes(p.q_tiles);
-  cudaError_t e = gen ? launch_pdl(tree_kernel<D, BF, true>, dim3(grid), kThreads, smem, s, tq, tk, tv, p)
-                      : launch_pdl(tree_kernel<D, BF, false>, dim3(grid), kThreads, smem, s, tq, tk, tv, p);
+  const int smem = TreeCfg<D>::smem_bytes(p.q_tiles, REP);
+  cudaError_t e = gen ? launch_pdl(tree_kernel<D, BF, true, REP>, dim3(grid), kThreads, smem, s, tq, tk, tv, p)
+                      : launch_pdl(tree_kernel<D, BF, false, REP>, dim3(grid), kThreads, smem, s, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(tree_join_kernel<D, BF>, dim3(4 * grid), D / 8 * 32, 0, s, p);
 }
 
-}  // namespace
-
-cudaError_t tree_configure(int head_size, int bf16) {
-  if (head_size == 64) return bf16 ? configure_db<64, true>() : configure_db<64, false>();
-  return bf16 ? configure_db<128, true>() : configure_db<128, false>();
+// One translation unit per head size (PA_TREE_D), so that they compile side by side.
+template <bool BF>
+cudaError_t configure_bf(int rep) {
+#if PA_TREE_D == 64
+  if (rep == 4) return configure_dbr<64, BF, 4>();
+  if (rep == 2) return configure_dbr<64, BF, 2>();
+#endif
+  return configure_dbr<PA_TREE_D, BF, 1>();
 }
 
-cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
-                        int bf16, int grid, cudaStream_t s) {
-  if (p.D == 64) return bf16 ? launch_db<64, true>(tq, tk, tv, p, grid, s) : launch_db<64, false>(tq, tk, tv, p, grid, s);
-  return bf16 ? launch_db<128, true>(tq, tk, tv, p, grid, s) : launch_db<128, false>(tq, tk, tv, p, grid, s);
+template <bool BF>
+cudaError_t launch_bf(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int grid,
+                      cudaStream_t s) {
+#if PA_TREE_D == 64
+  if (p.rep == 4) return launch_dbr<64, BF, 4>(tq, tk, tv, p, grid, s);
+  if (p.rep == 2) return launch_dbr<64, BF, 2>(tq, tk, tv, p, grid, s);
+#endif
+  return launch_dbr<PA_TREE_D, BF, 1>(tq, tk, tv, p, grid, s);
+}
+
+}  // namespace
+
+template <>
+cudaError_t tree_configure<PA_TREE_D>(int bf16, int rep) {
+  return bf16 ? configure_bf<true>(rep) : configure_bf<false>(rep);
+}
+
+template <>
+cudaError_t launch_tree<PA_TREE_D>(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const TreeParams& p, int bf16, int grid, cudaStream_t s) {
+  return bf16 ? launch_bf<true>(tq, tk, tv, p, grid, s) : launch_bf<false>(tq, tk, tv, p, grid, s);
 }
 
 }  // namespace pa
