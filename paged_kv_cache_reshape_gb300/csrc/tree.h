@@ -94,6 +94,7 @@ struct TreeParams {
   int batch, T;
   int H, Hk, G, D;
   int tile_tokens;           // tokens of a row tile (128 / rep rows)
+  int inv_pair;              // 2^20 / (2 tile_tokens), rounded up
   int bs, NB, MB, log_bs, log_page_rows, oob_row;
   int max_draft, words, max_kv;
   int window;

@@ -468,6 +468,7 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   p.scale = h->scale;
   p.softcap = c.softcap;
   p.tile_tokens = h->tile_tokens;
+  p.inv_pair = (1 << 20) / (2 * h->tile_tokens) + 1;
   const int page_rows = std::min(c.block_size, pa::kPrefillKeys);
   p.log_page_rows = 0;
   while ((1 << p.log_page_rows) < page_rows) ++p.log_page_rows;

@@ -74,6 +74,7 @@ constexpr int kMaskRing = 16;
 constexpr int kMaxSlots = 12;  // K/V ring slots at most
 constexpr int kJoinChannels = 16;  // channels of the replicas joined at a time
 constexpr int kUnitCost = 2;  // a unit's fixed cost in key tiles
+constexpr int kMinRange = 1;  // a line of less than twice this stays whole
 
 template <int D>
 struct TreeCfg {
@@ -172,7 +173,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bit
   } else if (s.n > 0) {
     s.lo = p.window >= 1 ? (max(0, s.past + 1 - p.window) & ~(kKeys - 1)) : 0;
     s.nt = (s.past + s.n - s.lo + kKeys - 1) / kKeys;
-    s.pairs = (s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+    s.pairs = (((s.n - 1) * p.inv_pair) >> 20) + 1;  // ceil(n / (2 tile_tokens))
     s.len = (s.nt + kUnitCost) * s.pairs;
   }
   return s;
@@ -232,30 +233,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-    mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], 4);
-      mbar_init(&ctl->o_done[i], 1);
-      mbar_init(&ctl->o_free[i], 8);
+  if (warp == 0) {  // the barriers, side by side
+    if (lane < 2) {
+      mbar_init(&ctl->s_full[lane], 1);
+      mbar_init(&ctl->p_full[lane], 4);
+      mbar_init(&ctl->o_done[lane], 1);
+      mbar_init(&ctl->o_free[lane], 8);
+      mbar_init(&ctl->join[lane], 4);
+    } else if (lane < 2 + kInfoRing) {
+      mbar_init(&ctl->info_full[lane - 2], 1);
+      mbar_init(&ctl->info_empty[lane - 2], 1 + 8 + 2);  // MMA, softmax and K/V producer warps
+    } else if (lane == 2 + kInfoRing) {
+      mbar_init(&ctl->q_full, 1);
+      mbar_init(&ctl->q_empty, 1);
+      mbar_init(&ctl->xchg_full, 8);
+      mbar_init(&ctl->xchg_done, 8);
+      mbar_init(&ctl->drain, 1);
+      ctl->abort = 0;
     }
-    for (int i = 0; i < kInfoRing; ++i) {
-      mbar_init(&ctl->info_full[i], 1);
-      mbar_init(&ctl->info_empty[i], 1 + 8 + 2);  // MMA, softmax and K/V producer warps
+    if (lane < kMaskRing) {
+      mbar_init(&ctl->mask_full[lane], 1);
+    } else if (lane < kMaskRing + kMaxSlots) {
+      mbar_init(&ctl->full[lane - kMaskRing], 1);
+      mbar_init(&ctl->empty[lane - kMaskRing], 1);
     }
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
-    }
-    for (int i = 0; i < kMaskRing; ++i) mbar_init(&ctl->mask_full[i], 1);
-    mbar_init(&ctl->xchg_full, 8);
-    mbar_init(&ctl->xchg_done, 8);
-    mbar_init(&ctl->join[0], 4);
-    mbar_init(&ctl->join[1], 4);
-    mbar_init(&ctl->drain, 1);
-    ctl->abort = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < 4 * kTreeMaxWords) ctl->bad[0][0][threadIdx.x] = 0;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // once the previous segment's S products are done.
       const uint32_t q_bytes = C::kChunks * p.G * p.tile_tokens * 128;  // of one box
       const int total = ctl->total;
-      const int n_ranges = min(p.n_ranges, total + 1);
+      const int n_ranges = min(p.n_ranges, total / kMinRange + 1);
       const int n_chunks = total > 0 ? n_ranges * p.Hk : 0;
       const int len_q = total / n_ranges, len_r = total - len_q * n_ranges;
       auto range_begin = [&](int i) -> int { return len_q * i + min(i, len_r); };  // the first len_r are one longer
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           f.live = 1;
           f.b = 32 * group + src;
+          if (lane == 0) prefetch_l1(p.block_table + (size_t)f.b * p.MB + ((s.lo + tile0 * kKeys) >> p.log_bs));
           f.k = chunk % p.Hk;
           f.t0 = s.t0 + u * 2 * p.tile_tokens;
           f.ntok = min(2 * p.tile_tokens, s.n - u * 2 * p.tile_tokens);
@@ -427,6 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+        }
+        if (f.live) {
+          // what the softmax warps will read of the unit's rows, towards L1
+          if (GEN && p.positions && 32 * lane < f.ntok) prefetch_l1(p.positions + f.t0 + 32 * lane);
+          if (GEN && p.slopes && lane == 31) prefetch_l1(p.slopes + f.k * p.G);
+          if (p.mask && f.key0 + f.nt * kKeys > f.past)
+            for (int i = 32 * lane; i < f.ntok * p.words; i += 1024) prefetch_l1(p.mask + (size_t)f.t0 * p.words + i);
         }
         if (lane == 0 && cut.rows > 0) p.cuts[atomicAdd(&p.counters->n_cuts, 1)] = cut;
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -641,12 +650,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.slopes && row_ok) slope2 = p.slopes[sg.k * p.G + (row - rj * p.G)] * kLog2e;
       }
       const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;  // no row admits a key below
-      if (p.mask && row_ok && sg.key0 + nt * kKeys > past) {
-        // the row's mask words, towards L1 for the tiles that hold draft tokens
-        const uint32_t* row = p.mask + (size_t)t * p.words;
-        prefetch_l1(row);
-        prefetch_l1(row + p.words - 1);
-      }
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int i = two ? 0 : X; i < nt; i += two ? 1 : 2) {
