@@ -431,8 +431,8 @@ PA_API pa_status pa_last_step_counts(pa_handle h, int32_t* counts);
  * pa_rotary is the same rotation on plain rows, and its gradient.
  *
  * Padding: rows at and behind cum[batch] (cum[batch] <= token_count) are
- * neither read nor written, so a captured step may be sized for more tokens
- * than it holds. */
+ * not written and what they hold does not matter, so a captured step may be
+ * sized for more tokens than it holds. */
 
 /* Element types of pa_rotary. */
 enum { PA_ROTARY_FP16 = 0, PA_ROTARY_BF16 = 1, PA_ROTARY_FP32 = 2 };
@@ -498,7 +498,7 @@ PA_API void pa_rotary_config_init(pa_rotary_config* rc);
  * outputs that overlap each other or the other input.  Overlap is decided by
  * whole ranges of rows, save that two slices of one row layout (equal
  * strides, disjoint columns) do not overlap.  num_heads or kv_num_heads 0
- * leaves that tensor out.  Runs on the current device; keeps nothing, so calls may overlap. */
+ * leaves that tensor out (at most 4096 of each).  Runs on the current device; keeps nothing, so calls may overlap. */
 PA_API pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int32_t* positions,
                            int token_count, int num_heads, const void* query, int64_t query_stride,
                            void* query_out, int64_t query_out_stride, int kv_num_heads, const void* key,
@@ -513,7 +513,7 @@ typedef struct pa_tree_handle_s* pa_tree_handle;
  * PA_CACHE_BF16, the activations' type too).  Its rotary fields are not read
  * here (positions are explicit; pa_tree_write takes a pa_rotary_config).
  * PA_NOT_SUPPORTED: head_size other than 64 and 128, 8-bit caches, the latent
- * layout, packed_qkv, qk_norm.  Allocates the workspace (split-KV partials,
+ * layout, packed_qkv, qk_norm, more than 4096 heads.  Allocates the workspace (split-KV partials,
  * error word) on the current device.
  * One handle's pa_tree_attention calls share that workspace: calls (and
  * replays of graphs captured from them) on one handle must not overlap on the

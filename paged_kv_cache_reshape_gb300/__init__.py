@@ -432,15 +432,16 @@ def rotary_steps_tensor(steps, device="cuda"):
 
 
 def _row_stride(t):
-    if t.stride(-1) != 1 or t.dim() != 2:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise PAError(PA_INVALID_ARGUMENT, "rows must be 2-D with contiguous columns")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return stride[0] if len(t) > 1 else 0
 
 
 def pa_rotary(rc, steps, positions, token_count, num_heads, query, query_out, kv_num_heads=0, key=None,
               key_out=None, stream=None):
     """Rotates the rows of query [T, num_heads * D] and key; row strides are the tensors' own."""
-    st = lib().pa_rotary(rc, steps.data_ptr(), positions.data_ptr(), token_count, num_heads,
+    st = (_lib or lib()).pa_rotary(rc, steps.data_ptr(), positions.data_ptr(), token_count, num_heads,
                          query.data_ptr() if num_heads else None, _row_stride(query) if num_heads else 0,
                          query_out.data_ptr() if num_heads else None, _row_stride(query_out) if num_heads else 0,
                          kv_num_heads, key.data_ptr() if kv_num_heads else None,
@@ -467,7 +468,7 @@ def pa_tree_destroy(h):
 
 def pa_tree_write(h, rc, steps, positions, query, key, value, query_out, key_cache, value_cache, block_table,
                   cumulative_sequence_lengths, past_sequence_lengths, batch, token_count, stream=None):
-    st = lib().pa_tree_write(h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query),
+    st = (_lib or lib()).pa_tree_write(h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query),
                              key.data_ptr(), _row_stride(key), value.data_ptr(), _row_stride(value),
                              query_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                              block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
@@ -483,7 +484,7 @@ def pa_tree_attention(h, query, key_cache, value_cache, block_table, cumulative_
                        None if tree_mask is None else tree_mask.data_ptr(),
                        None if distance_slopes is None else distance_slopes.data_ptr(),
                        None if head_sink is None else head_sink.data_ptr())
-    st = lib().pa_tree_attention(h, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+    st = (_lib or lib()).pa_tree_attention(h, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                  block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
                                  past_sequence_lengths.data_ptr(), batch, token_count, x, output.data_ptr(), stream)
     if st:
@@ -505,7 +506,7 @@ class layer_pools:
 def pa_tree_commit(h, layers, block_table, past_sequence_lengths, accepted, accepted_count, batch, new_past=None,
                    stream=None):
     """accepted [batch, max_accepted] int32 (contiguous), accepted_count [batch]; layers: a layer_pools."""
-    st = lib().pa_tree_commit(h, layers.keys, layers.values, layers.num_layers, block_table.data_ptr(),
+    st = (_lib or lib()).pa_tree_commit(h, layers.keys, layers.values, layers.num_layers, block_table.data_ptr(),
                               past_sequence_lengths.data_ptr(), accepted.data_ptr(), accepted_count.data_ptr(),
                               accepted.shape[1], batch, None if new_past is None else new_past.data_ptr(), stream)
     if st:

@@ -21,6 +21,7 @@ bool encode_rows_map(CUtensorMap* m, const void* base, int D, int heads_total, l
 bool encode_groups_map(CUtensorMap* m, const void* base, int D, int Hk, long long rows_total, int rows_box);
 
 // ---- rotary (rotary.cu)
+constexpr int kRotaryMaxHeads = 4096;
 struct RotaryRows {  // rows of one tensor; nheads == 0: absent
   const void* src;
   void* dst;           // NULL for rows that go to the pool
@@ -77,7 +78,7 @@ struct Cut {
 };
 
 struct TreeCounters {  // zero between calls
-  int n_cuts;
+  int n_cuts[2];  // units in two pieces, in more
   int joined;   // blocks of the joining kernel that are done
 };
 

@@ -7,8 +7,9 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
+#include <new>
 #include <string>
-#include <vector>
 
 #include "../../include/pa.h"
 #include "step.h"
@@ -232,8 +233,8 @@ pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int
   pa_status st = check_rotary(nullptr, rc);
   if (st != PA_OK) return st;
   if (token_count < 0) return pa::host_fail(PA_INVALID_ARGUMENT, "token_count must be >= 0 (got %d)", token_count);
-  if (num_heads < 0 || kv_num_heads < 0 || num_heads > 65536 || kv_num_heads > 65536)
-    return pa::host_fail(PA_INVALID_ARGUMENT, "num_heads and kv_num_heads must be in [0, 65536] (got %d, %d)",
+  if (num_heads < 0 || kv_num_heads < 0 || num_heads > pa::kRotaryMaxHeads || kv_num_heads > pa::kRotaryMaxHeads)
+    return pa::host_fail(PA_INVALID_ARGUMENT, "num_heads and kv_num_heads must be in [0, 4096] (got %d, %d)",
                          num_heads, kv_num_heads);
   if (token_count == 0 || num_heads + kv_num_heads == 0) return PA_OK;
   if (!steps || !aligned(steps, 8))
@@ -283,11 +284,14 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
     return pa::host_fail(PA_NOT_SUPPORTED, "trees are built for separate K and V caches (kv_cache_layout SEPARATE)");
   if (c.cache_dtype != PA_CACHE_FP16 && c.cache_dtype != PA_CACHE_BF16)
     return pa::host_fail(PA_NOT_SUPPORTED, "trees are built for a cache_dtype of fp16 or bfloat16");
+  if (c.num_heads > pa::kRotaryMaxHeads)
+    return pa::host_fail(PA_NOT_SUPPORTED, "trees are built for num_heads <= %d (got %d)", pa::kRotaryMaxHeads, c.num_heads);
   if (c.packed_qkv || c.qk_norm)
     return pa::host_fail(PA_NOT_SUPPORTED, "trees take neither packed_qkv nor qk_norm");
   if (c.head_size != 64 && c.head_size != 128)
     return pa::host_fail(PA_NOT_SUPPORTED, "trees are built for head_size 64 and 128 (got %d)", c.head_size);
-  pa_tree_handle h = new pa_tree_handle_s();
+  pa_tree_handle h = new (std::nothrow) pa_tree_handle_s();
+  if (!h) return pa::host_fail(PA_CUDA_ERROR, "pa_tree_create: out of host memory");
   h->cfg = *cfg;
   h->max_draft = max_draft_tokens;
   h->words = (max_draft_tokens + 31) / 32;
@@ -297,6 +301,10 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   h->max_kv = c.max_kv_len_bound > 0 ? std::min(c.max_kv_len_bound, kv_cap) : kv_cap;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+  if (e != cudaSuccess) {
+    delete h;
+    return tree_cuda_fail(nullptr, e, "pa_tree_create");
+  }
   // Workspace: error word, counters, the cut units, the starts of the groups
   // of sequences (per CTA) and two partial results per chunk (256-byte
   // aligned pieces).
@@ -529,19 +537,19 @@ pa_status pa_tree_commit(pa_tree_handle h, void* const* key_caches, void* const*
       return tree_fail(h, PA_INVALID_ARGUMENT, "new_past must not overlap past_sequence_lengths, accepted or accepted_count");
   // Pools: present, aligned and apart from one another.
   const uintptr_t bytes = (uintptr_t)c.num_blocks * c.block_size * c.kv_num_heads * c.head_size * 2;
-  std::vector<uintptr_t> at;
-  at.reserve(2 * (size_t)num_layers);
+  std::unique_ptr<uintptr_t[]> store(new (std::nothrow) uintptr_t[2 * (size_t)num_layers]);
+  if (!store) return tree_fail(h, PA_CUDA_ERROR, "pa_tree_commit: out of host memory");
+  uintptr_t *at = store.get(), *end = at;
   for (int l = 0; l < num_layers; ++l) {
     for (void* q : {key_caches[l], value_caches[l]}) {
       if (!q || !aligned(q, 16))
         return tree_fail(h, PA_INVALID_ARGUMENT, "layer %d: key_cache and value_cache must be 16-byte aligned device pointers", l);
-      at.push_back(reinterpret_cast<uintptr_t>(q));
+      *end++ = reinterpret_cast<uintptr_t>(q);
     }
   }
-  if (!std::is_sorted(at.begin(), at.end())) std::sort(at.begin(), at.end());
-  for (size_t i = 1; i < at.size(); ++i)
-    if (at[i] - at[i - 1] < bytes)
-      return tree_fail(h, PA_INVALID_ARGUMENT, "two of the pools overlap");
+  if (!std::is_sorted(at, end)) std::sort(at, end);
+  for (uintptr_t* q = at + 1; q < end; ++q)
+    if (q[0] - q[-1] < bytes) return tree_fail(h, PA_INVALID_ARGUMENT, "two of the pools overlap");
   OnDevice g(h->device);
   pa::CommitParams p{};
   p.row_vecs = c.kv_num_heads * c.head_size / 8;

@@ -74,7 +74,7 @@ constexpr int kMaskRing = 16;
 constexpr int kMaxSlots = 12;  // K/V ring slots at most
 constexpr int kJoinChannels = 16;  // channels of the replicas joined at a time
 constexpr int kUnitCost = 2;  // a unit's fixed cost in key tiles
-constexpr int kMinRange = 1;  // a line of less than twice this stays whole
+constexpr int kMinRange = 2;  // a line of less than twice this stays whole
 
 template <int D>
 struct TreeCfg {
@@ -437,7 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.mask && f.key0 + f.nt * kKeys > f.past)
             for (int i = 32 * lane; i < f.ntok * p.words; i += 1024) prefetch_l1(p.mask + (size_t)f.t0 * p.words + i);
         }
-        if (lane == 0 && cut.rows > 0) p.cuts[atomicAdd(&p.counters->n_cuts, 1)] = cut;
+        if (lane == 0 && cut.rows > 0) {  // units in two pieces from the front, in more from the back
+          const int many = cut.more > 1, at = atomicAdd(&p.counters->n_cuts[many], 1);
+          p.cuts[many ? p.n_ranges * p.Hk - 1 - at : at] = cut;
+        }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok || !f.live) break;
       }
@@ -1040,69 +1043,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partial results of the units that range borders cut.  A warp
-// takes 8 rows and 8 channels of a unit, its lanes the rows times four shares
-// of the partials (every fourth one), whose loads are then in flight at once;
-// the shares are added by shuffles.  Partials are stored channel group by
-// channel group with rows side by side, so both kernels access whole
-// sectors.  The last block to finish clears the counters.
-constexpr int kJoinRows = 8;
+// Joins the partial results of the units that range borders cut; a warp takes
+// 8 channels of some rows.  Units in two pieces (the front of the list of
+// cuts): 32 rows at a time, a lane is a row and loads both at once.  Units in
+// more pieces (the back of the list): 8 rows at a time times four shares of
+// the pieces (every fourth one), added by shuffles.  Partials are stored
+// channel group by channel group with rows side by side, so both kernels
+// access whole sectors.  The last block to finish clears the counters.
 template <int D, bool BF>
 __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  const int lane = threadIdx.x & 31, c8 = threadIdx.x >> 5, share = lane >> 3;
-  const int row_groups = p.part_rows / kJoinRows;
+  const int lane = threadIdx.x & 31, c8 = threadIdx.x >> 5;
+  const int groups2 = p.part_rows / 32, groups = p.part_rows / 8;
   griddep_wait();
   griddep_launch_dependents();
-  // the first cut is read beside the count (entries behind it are stale, not used)
-  Cut cut = p.cuts[min((int)blockIdx.x / row_groups, p.n_ranges * p.Hk - 1)];
-  const int n_work = p.counters->n_cuts * row_groups;
-  for (int i = blockIdx.x; i < n_work; i += gridDim.x) {
-    if (i != (int)blockIdx.x) cut = p.cuts[i / row_groups];
-    const int row = i % row_groups * kJoinRows + (lane & 7);
-    if (row - (lane & 7) >= cut.rows) continue;
-    const int ns = cut.more + 1;
-    auto slot_of = [&](int s) -> size_t { return s == 0 ? cut.slot0 : cut.slot1 + 2 * p.Hk * (s - 1); };
-    float m = -INFINITY, den = 0.f, acc[8] = {};
-#pragma unroll 2
-    for (int s = share; s < ns; s += 4) {
-      const size_t at = slot_of(s);
-      const float2 ml = p.part_ml[at * p.part_rows + row];
-      const float4* o = p.part_o + (at * (D / 4) + 2 * c8) * p.part_rows + row;
-      const float4 a = o[0], b = o[p.part_rows];
-      if (ml.x == -INFINITY) continue;
-      const float m_new = fmaxf(m, ml.x), f_old = ex2(m - m_new), f = ex2(ml.x - m_new);
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      den = m == -INFINITY ? ml.y * f : den * f_old + ml.y * f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = m == -INFINITY ? v[e] * f : acc[e] * f_old + v[e] * f;
-      m = m_new;
-    }
-    float M = m;
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-    const float f = m == -INFINITY ? 0.f : ex2(m - M);
-    den = f == 0.f ? 0.f : den * f;
-    den += __shfl_xor_sync(0xffffffffu, den, 8);
-    den += __shfl_xor_sync(0xffffffffu, den, 16);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      acc[e] = f == 0.f ? 0.f : acc[e] * f;
-      acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 8);
-      acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
-    }
+  const int n2 = p.counters->n_cuts[0] * groups2, n_work = n2 + p.counters->n_cuts[1] * groups;
+  const int last = p.n_ranges * p.Hk - 1;  // of the list
+  Cut cut{};
+  // out = acc / (den + sink) of one row
+  auto store = [&](int row, float m, float den, const float* acc) {
     const int X = row / kRows, r = row - X * kRows, rj = r / p.G, j = X * p.tile_tokens + rj;
-    if (share != 0 || row >= cut.rows || rj >= p.tile_tokens || j >= cut.ntok) continue;
+    if (row >= cut.rows || rj >= p.tile_tokens || j >= cut.ntok) return;
     const int t = cut.t0 + j, h = cut.k * p.G + (r - rj * p.G);
-    if (p.head_sink && M != -INFINITY) den += ex2(elem16_to_float(p.head_sink[h], BF) * kLog2e - M);
+    if (p.head_sink && m != -INFINITY) den += ex2(elem16_to_float(p.head_sink[h], BF) * kLog2e - m);
     const float inv = den == 0.f ? 0.f : 1.f / den;
     *reinterpret_cast<uint4*>(p.out + ((size_t)t * p.H + h) * D + 8 * c8) =
         make_uint4(pack2<BF>(acc[0] * inv, acc[1] * inv), pack2<BF>(acc[2] * inv, acc[3] * inv),
                    pack2<BF>(acc[4] * inv, acc[5] * inv), pack2<BF>(acc[6] * inv, acc[7] * inv));
+  };
+  for (int i = blockIdx.x; i < n_work; i += gridDim.x) {
+    if (i < n2) {
+      cut = p.cuts[i / groups2];
+      const int row = i % groups2 * 32 + lane;
+      if (row - lane >= cut.rows) continue;
+      const size_t at0 = cut.slot0, at1 = cut.slot1;
+      const float4* o0 = p.part_o + (at0 * (D / 4) + 2 * c8) * p.part_rows + row;
+      const float4* o1 = p.part_o + (at1 * (D / 4) + 2 * c8) * p.part_rows + row;
+      const float2 ml0 = p.part_ml[at0 * p.part_rows + row], ml1 = p.part_ml[at1 * p.part_rows + row];
+      const float4 a0 = o0[0], b0 = o0[p.part_rows], a1 = o1[0], b1 = o1[p.part_rows];
+      const float m = fmaxf(ml0.x, ml1.x);
+      const float f0 = ml0.x == -INFINITY ? 0.f : ex2(ml0.x - m), f1 = ml1.x == -INFINITY ? 0.f : ex2(ml1.x - m);
+      const float v0[8] = {a0.x, a0.y, a0.z, a0.w, b0.x, b0.y, b0.z, b0.w};
+      const float v1[8] = {a1.x, a1.y, a1.z, a1.w, b1.x, b1.y, b1.z, b1.w};
+      float acc[8], den = f0 == 0.f ? 0.f : f0 * ml0.y;
+      if (f1 != 0.f) den += f1 * ml1.y;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[e] = f0 == 0.f ? 0.f : f0 * v0[e];
+        if (f1 != 0.f) acc[e] += f1 * v1[e];
+      }
+      store(row, m, den, acc);
+    } else {
+      cut = p.cuts[last - (i - n2) / groups];
+      const int row = (i - n2) % groups * 8 + (lane & 7), ns = cut.more + 1;
+      if (row - (lane & 7) >= cut.rows) continue;
+      auto slot_of = [&](int s) -> size_t { return s == 0 ? cut.slot0 : cut.slot1 + 2 * p.Hk * (s - 1); };
+      float m = -INFINITY, den = 0.f, acc[8] = {};
+#pragma unroll 2
+      for (int s = lane >> 3; s < ns; s += 4) {
+        const size_t at = slot_of(s);
+        const float2 ml = p.part_ml[at * p.part_rows + row];
+        const float4* o = p.part_o + (at * (D / 4) + 2 * c8) * p.part_rows + row;
+        const float4 a = o[0], b = o[p.part_rows];
+        if (ml.x == -INFINITY) continue;
+        const float m_new = fmaxf(m, ml.x), f_old = m == -INFINITY ? 0.f : ex2(m - m_new), f = ex2(ml.x - m_new);
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        den = f_old == 0.f ? ml.y * f : den * f_old + ml.y * f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = f_old == 0.f ? v[e] * f : acc[e] * f_old + v[e] * f;
+        m = m_new;
+      }
+      float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+      const float f = m == -INFINITY ? 0.f : ex2(m - M);
+      den = f == 0.f ? 0.f : den * f;
+      den += __shfl_xor_sync(0xffffffffu, den, 8);
+      den += __shfl_xor_sync(0xffffffffu, den, 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[e] = f == 0.f ? 0.f : acc[e] * f;
+        acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 8);
+        acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
+      }
+      if (lane < 8) store(row, M, den, acc);
+    }
   }
   if (threadIdx.x == 0) {  // (n_cuts was read above)
     __threadfence();
     if (atomicAdd(&p.counters->joined, 1) == (int)gridDim.x - 1) {
-      p.counters->n_cuts = 0;
+      p.counters->n_cuts[0] = 0;
+      p.counters->n_cuts[1] = 0;
       p.counters->joined = 0;
     }
   }
@@ -1134,7 +1163,7 @@ cudaError_t launch_dbr(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   cudaError_t e = gen ? launch_pdl(tree_kernel<D, BF, true, REP>, dim3(grid), kThreads, smem, s, tq, tk, tv, p)
                       : launch_pdl(tree_kernel<D, BF, false, REP>, dim3(grid), kThreads, smem, s, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_join_kernel<D, BF>, dim3(4 * grid), D / 8 * 32, 0, s, p);
+  return launch_pdl(tree_join_kernel<D, BF>, dim3(2 * grid), D / 8 * 32, 0, s, p);
 }
 
 // One translation unit per head size (PA_TREE_D), so that they compile side by side.

@@ -81,7 +81,8 @@ def rotary(rc=None, **over):
 
 
 @pytest.mark.parametrize("over,word", [
-    (dict(token_count=-1), "token_count"), (dict(num_heads=-1), "num_heads"), (dict(steps=None), "steps"),
+    (dict(token_count=-1), "token_count"), (dict(num_heads=-1), "num_heads"),
+    (dict(kv_num_heads=4097), "kv_num_heads"), (dict(steps=None), "steps"),
     (dict(steps=A + 4), "steps"), (dict(positions=None), "positions"), (dict(query=None), "query"),
     (dict(query=A + 8), "query"), (dict(query_out=None), "query_out"), (dict(key=None), "key"),
     (dict(key_out=None), "key_out"), (dict(query_stride=120), "query"), (dict(query_stride=132), "query"),
