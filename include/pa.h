@@ -492,7 +492,7 @@ PA_API void pa_rotary_config_init(pa_rotary_config* rc);
  *   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a)
  * in fp32, rounded once to the type; the other channels are copied.
  * Row t of a tensor starts at t * stride elements (a multiple of 8, at least
- * heads * D; 0 => heads * D), so slices of packed rows are taken and written
+ * heads * D; 0 => heads * D; one row has no stride), so slices of packed rows are taken and written
  * in place.  query_out == query with equal strides rotates in place; an
  * output that overlaps its input in any other way is refused, and so are
  * outputs that overlap each other or the other input.  Overlap is decided by

@@ -435,7 +435,7 @@ def _row_stride(t):
     stride = t.stride()
     if len(stride) != 2 or stride[1] != 1:
         raise PAError(PA_INVALID_ARGUMENT, "rows must be 2-D with contiguous columns")
-    return stride[0] if len(t) > 1 else 0
+    return stride[0]
 
 
 def pa_rotary(rc, steps, positions, token_count, num_heads, query, query_out, kv_num_heads=0, key=None,

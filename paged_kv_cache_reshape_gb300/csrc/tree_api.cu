@@ -106,9 +106,10 @@ pa_status check_rotary(pa_tree_handle h, const pa_rotary_config* rc) {
   return PA_OK;
 }
 
-// One tensor of a rotation; *stride is set to the dense one when 0.
-pa_status check_rows(pa_tree_handle h, const char* name, const void* p, int heads, int D, int64_t* stride) {
-  if (*stride == 0) *stride = (int64_t)heads * D;
+// One tensor of a rotation; *stride is set to the dense one when 0, or when
+// there is one row only.
+pa_status check_rows(pa_tree_handle h, const char* name, const void* p, int T, int heads, int D, int64_t* stride) {
+  if (*stride == 0 || T == 1) *stride = (int64_t)heads * D;
   if (!p) return tree_fail(h, PA_INVALID_ARGUMENT, "%s must not be NULL", name);
   if (!aligned(p, 16)) return tree_fail(h, PA_INVALID_ARGUMENT, "%s must be 16-byte aligned", name);
   if (*stride < (int64_t)heads * D || *stride % 8 || *stride > (INT64_C(1) << 40))
@@ -249,8 +250,8 @@ pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int
   Rows in[2], out[2];
   for (int i = 0; i < 2; ++i) {
     if (t[i].heads == 0) continue;
-    if ((st = check_rows(nullptr, t[i].in, t[i].src, t[i].heads, D, &t[i].ss)) != PA_OK) return st;
-    if ((st = check_rows(nullptr, t[i].out, t[i].dst, t[i].heads, D, &t[i].ds)) != PA_OK) return st;
+    if ((st = check_rows(nullptr, t[i].in, t[i].src, token_count, t[i].heads, D, &t[i].ss)) != PA_OK) return st;
+    if ((st = check_rows(nullptr, t[i].out, t[i].dst, token_count, t[i].heads, D, &t[i].ds)) != PA_OK) return st;
     in[i] = Rows{t[i].src, token_count, t[i].ss * e, (long long)t[i].heads * D * e};
     out[i] = Rows{t[i].dst, token_count, t[i].ds * e, (long long)t[i].heads * D * e};
     if (!same(in[i], out[i]) && overlap(in[i], out[i]))
@@ -387,10 +388,10 @@ pa_status pa_tree_write(pa_tree_handle h, const pa_rotary_config* rc, const uint
     return tree_fail(h, PA_INVALID_ARGUMENT, "positions must be a 4-byte aligned device pointer");
   const int H = c.num_heads, Hk = c.kv_num_heads, D = c.head_size;
   int64_t out_stride = 0;
-  if ((st = check_rows(h, "query", query, H, D, &query_stride)) != PA_OK ||
-      (st = check_rows(h, "key", key, Hk, D, &key_stride)) != PA_OK ||
-      (st = check_rows(h, "value", value, Hk, D, &value_stride)) != PA_OK ||
-      (st = check_rows(h, "query_out", query_out, H, D, &out_stride)) != PA_OK)
+  if ((st = check_rows(h, "query", query, token_count, H, D, &query_stride)) != PA_OK ||
+      (st = check_rows(h, "key", key, token_count, Hk, D, &key_stride)) != PA_OK ||
+      (st = check_rows(h, "value", value, token_count, Hk, D, &value_stride)) != PA_OK ||
+      (st = check_rows(h, "query_out", query_out, token_count, H, D, &out_stride)) != PA_OK)
     return st;
   const Rows qi{query, token_count, query_stride * 2, (long long)H * D * 2};
   const Rows qo{query_out, token_count, out_stride * 2, (long long)H * D * 2};

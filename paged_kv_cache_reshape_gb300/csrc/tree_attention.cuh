@@ -264,39 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kKWarp && lane == 0) prefetch_tmap(&tm_k);
   if (warp == kVWarp && lane == 0) prefetch_tmap(&tm_v);
 
-  griddep_wait();  // lengths, queries and pools may come from the previous kernel
-  griddep_launch_dependents();
-
-  // Where each group of 32 sequences starts in the line, and its length.
-  int* const groups = p.batch <= kThreads ? ctl->scan : p.groups + (size_t)blockIdx.x * p.n_groups;
-  int bits = 0;
-  long long before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    long long len = b < p.batch ? seq_work(p, b, bits).len : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) len += __shfl_xor_sync(0xffffffffu, len, o);
-    // (no sum over a line of at most 2^31 - 1 wraps; a longer one is refused below)
-    __syncthreads();
-    if (lane == 0) ctl->scan[warp] = (int)min(len, 0x7fffffffll);
-    __syncthreads();
-    long long first = before;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) first += ctl->scan[w];
-      before += ctl->scan[w];
-    }
-    if (p.batch <= kThreads) __syncthreads();  // the groups' starts replace their lengths
-    if (lane == 0 && (b0 >> 5) + warp < p.n_groups) groups[(b0 >> 5) + warp] = (int)first;
-  }
-  if (before > 0x7fffffffll) {  // 2^31 key tiles: days of work
-    bits |= PA_DEVERR_KV_BOUND;
-    before = 0;
-  }
-  if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
-  if (threadIdx.x == 0) ctl->total = (int)before;
   if ((smem_u32(smem) & 1023) != 0) {  // the swizzled operands need it; never seen
-    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+    if (threadIdx.x == 0) note_timeout(p.err, p.err_site, kSiteTree);
     return;
   }
   if (warp == kMmaWarp) {
@@ -307,6 +276,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+
+  griddep_wait();  // lengths, queries and pools may come from the previous kernel
+  griddep_launch_dependents();
+
+  // Where each group of 32 sequences starts in the line, and its length (a
+  // batch of one group is left to the fetcher).
+  int* const groups = p.batch <= kThreads ? ctl->scan : p.groups + (size_t)blockIdx.x * p.n_groups;
+  if (p.n_groups > 1) {
+    int bits = 0;
+    long long before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      long long len = b < p.batch ? seq_work(p, b, bits).len : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) len += __shfl_xor_sync(0xffffffffu, len, o);
+      // (no sum over a line of at most 2^31 - 1 wraps; a longer one is refused below)
+      __syncthreads();
+      if (lane == 0) ctl->scan[warp] = (int)min(len, 0x7fffffffll);
+      __syncthreads();
+      long long first = before;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) first += ctl->scan[w];
+        before += ctl->scan[w];
+      }
+      if (p.batch <= kThreads) __syncthreads();  // the groups' starts replace their lengths
+      if (lane == 0 && (b0 >> 5) + warp < p.n_groups) groups[(b0 >> 5) + warp] = (int)first;
+    }
+    if (before > 0x7fffffffll) {  // 2^31 key tiles: days of work
+      bits |= PA_DEVERR_KV_BOUND;
+      before = 0;
+    }
+    if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
+    if (threadIdx.x == 0) ctl->total = (int)before;
+    __syncthreads();
+  }
   const int log_r = p.log_page_rows;  // log2(min(block_size, 128))
   const int pages = kKeys >> log_r;
 
@@ -319,19 +324,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Takes chunks, publishes their segments and loads a segment's Q tiles
       // once the previous segment's S products are done.
       const uint32_t q_bytes = C::kChunks * p.G * p.tile_tokens * 128;  // of one box
-      const int total = ctl->total;
+      // A window of 32 sequences, one per lane: where each ends in the line.
+      int group = -1, win_lo = 0, win_hi = 0, seq_end = 0;
+      SeqWork mine{};
+      auto load_window = [&](int& bits) {
+        const int b = 32 * group + lane;
+        mine = SeqWork{};
+        if (b < p.batch) mine = seq_work(p, b, bits);
+        seq_end = mine.len;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, seq_end, o);
+          if (lane >= o) seq_end += up;
+        }
+        seq_end += win_lo;
+        win_hi = __shfl_sync(0xffffffffu, seq_end, 31);
+      };
+      int ignored = 0, total;
+      if (p.n_groups > 1) {
+        total = ctl->total;
+      } else {
+        int bits = 0;
+        group = 0;
+        load_window(bits);
+        // (32 lengths below 2^26 cannot pass 2^31; a longer one is days of work)
+        if (__reduce_max_sync(0xffffffffu, (unsigned)mine.len) >= 1u << 26) {
+          bits |= PA_DEVERR_KV_BOUND;
+          win_hi = 0;
+        }
+        if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
+        total = win_hi;
+      }
       const int n_ranges = min(p.n_ranges, total / kMinRange + 1);
       const int n_chunks = total > 0 ? n_ranges * p.Hk : 0;
       const int len_q = total / n_ranges, len_r = total - len_q * n_ranges;
       auto range_begin = [&](int i) -> int { return len_q * i + min(i, len_r); };  // the first len_r are one longer
-      // A window of 32 sequences, one per lane: where each ends in the line.
-      int group = -1;
-      int win_lo = 0, win_hi = 0, seq_end = 0;
-      SeqWork mine{};
-      int ignored = 0;
-      uint32_t q_loads = 0;
       int chunk = (int)blockIdx.x - (int)gridDim.x, range = 0;
       int r = 0, r_begin = 0, r_end = 0;
+      uint32_t q_loads = 0;
       for (uint32_t tt = 0;; ++tt) {
         Segment f{};
         Cut cut{};
@@ -354,17 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             group = at > 0 ? g0 + at - 1 : g0 - 1;
             win_lo = groups[group];
-            const int b = 32 * group + lane;
-            mine = SeqWork{};
-            if (b < p.batch) mine = seq_work(p, b, ignored);
-            seq_end = mine.len;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int up = __shfl_up_sync(0xffffffffu, seq_end, o);
-              if (lane >= o) seq_end += up;
-            }
-            seq_end += win_lo;
-            win_hi = __shfl_sync(0xffffffffu, seq_end, 31);
+            load_window(ignored);
           }
           const int src = __ffs(__ballot_sync(0xffffffffu, r < seq_end)) - 1;
           SeqWork s;
