@@ -512,7 +512,7 @@ typedef struct pa_tree_handle_s* pa_tree_handle;
  * max_tokens, max_kv_len_bound and cache_dtype (PA_CACHE_FP16 or
  * PA_CACHE_BF16, the activations' type too).  Its rotary fields are not read
  * here (positions are explicit; pa_tree_write takes a pa_rotary_config).
- * PA_NOT_SUPPORTED: head_size other than 64 and 128, 8-bit caches, the latent
+ * PA_NOT_SUPPORTED: 8-bit caches, the latent
  * layout, packed_qkv, qk_norm, more than 4096 heads.  Allocates the workspace (split-KV partials,
  * error word) on the current device.
  * One handle's pa_tree_attention calls share that workspace: calls (and

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa_gb300.so")
 SOURCES = ["api.cu", "cache_write.cu", "decode.cu", "combine.cu", "prefill.cu", "prefill_pair.cu", "mla.cu",
-           "mla_tc.cu", "rotary.cu", "tree_api.cu", "tree_commit.cu", "tree_attention_64.cu", "tree_attention_128.cu"]
+           "mla_tc.cu", "rotary.cu", "tree_api.cu", "tree_commit.cu", "tree_attention_64.cu", "tree_attention_128.cu", "tree_attention_256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

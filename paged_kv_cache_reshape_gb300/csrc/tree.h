@@ -95,7 +95,8 @@ struct TreeParams {
   int batch, T;
   int H, Hk, G, D;
   int tile_tokens;           // tokens of a row tile (128 / rep rows)
-  int inv_pair;              // 2^20 / (2 tile_tokens), rounded up
+  int unit_tokens;           // tokens of a unit: two row tiles, or one (head_size 256)
+  int inv_unit;              // 2^20 / unit_tokens, rounded up
   int bs, NB, MB, log_bs, log_page_rows, oob_row;
   int max_draft, words, max_kv;
   int window;
@@ -121,9 +122,12 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
                         int bf16, int grid, cudaStream_t s);
 template <> cudaError_t tree_configure<64>(int, int);
 template <> cudaError_t tree_configure<128>(int, int);
+template <> cudaError_t tree_configure<256>(int, int);
 template <> cudaError_t launch_tree<64>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const TreeParams&,
                                         int, int, cudaStream_t);
 template <> cudaError_t launch_tree<128>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const TreeParams&,
+                                         int, int, cudaStream_t);
+template <> cudaError_t launch_tree<256>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const TreeParams&,
                                          int, int, cudaStream_t);
 
 }  // namespace pa

@@ -289,8 +289,6 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
     return pa::host_fail(PA_NOT_SUPPORTED, "trees are built for num_heads <= %d (got %d)", pa::kRotaryMaxHeads, c.num_heads);
   if (c.packed_qkv || c.qk_norm)
     return pa::host_fail(PA_NOT_SUPPORTED, "trees take neither packed_qkv nor qk_norm");
-  if (c.head_size != 64 && c.head_size != 128)
-    return pa::host_fail(PA_NOT_SUPPORTED, "trees are built for head_size 64 and 128 (got %d)", c.head_size);
   pa_tree_handle h = new (std::nothrow) pa_tree_handle_s();
   if (!h) return pa::host_fail(PA_CUDA_ERROR, "pa_tree_create: out of host memory");
   h->cfg = *cfg;
@@ -317,8 +315,13 @@ pa_status pa_tree_create(const pa_config* cfg, int max_draft_tokens, pa_tree_han
   h->rep = c.head_size == 64 ? (rows <= 32 ? 4 : rows <= 64 ? 2 : 1) : 1;
   h->tile_tokens = pa::kPrefillRows / h->rep / G;
   if (e == cudaSuccess)
-    e = c.head_size == 64 ? pa::tree_configure<64>(h->bf16, h->rep) : pa::tree_configure<128>(h->bf16, h->rep);
-  h->part_rows = max_draft_tokens > h->tile_tokens ? 2 * pa::kPrefillRows : (max_draft_tokens * G + 31) / 32 * 32;
+    e = c.head_size == 64    ? pa::tree_configure<64>(h->bf16, h->rep)
+        : c.head_size == 128 ? pa::tree_configure<128>(h->bf16, h->rep)
+                             : pa::tree_configure<256>(h->bf16, h->rep);
+  // rows of a unit: two row tiles at most, one at head_size 256
+  h->part_rows = max_draft_tokens <= h->tile_tokens ? (max_draft_tokens * G + 31) / 32 * 32
+                 : c.head_size == 256               ? pa::kPrefillRows
+                                                    : 2 * pa::kPrefillRows;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   h->n_ranges = pick_ranges(h->num_sms, c.kv_num_heads);
   const size_t chunks = (size_t)h->n_ranges * c.kv_num_heads, D = c.head_size;
@@ -477,14 +480,15 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   p.scale = h->scale;
   p.softcap = c.softcap;
   p.tile_tokens = h->tile_tokens;
-  p.inv_pair = (1 << 20) / (2 * h->tile_tokens) + 1;
-  const int page_rows = std::min(c.block_size, pa::kPrefillKeys);
+  p.unit_tokens = D == 256 ? h->tile_tokens : 2 * h->tile_tokens;
+  p.inv_unit = (1 << 20) / p.unit_tokens + 1;
+  const int page_rows = std::min(c.block_size, D == 256 ? 64 : 128);  // of a key tile
   p.log_page_rows = 0;
   while ((1 << p.log_page_rows) < page_rows) ++p.log_page_rows;
   p.oob_row = c.num_blocks * c.block_size;
   p.n_ranges = h->n_ranges;
   p.rep = h->rep;
-  p.q_tiles = h->max_draft > h->tile_tokens ? 2 : 1;
+  p.q_tiles = D != 256 && h->max_draft > h->tile_tokens ? 2 : 1;
   p.counters = h->counters;
   p.groups = h->groups;
   p.n_groups = (batch + 31) / 32;
@@ -500,8 +504,9 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
       !pa::encode_groups_map(&tv, value_cache, D, Hk, (long long)c.num_blocks * c.block_size, page_rows))
     return tree_fail(h, PA_CUDA_ERROR, "cuTensorMapEncodeTiled failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = D == 64 ? pa::launch_tree<64>(tq, tk, tv, p, h->bf16, h->num_sms, s)
-                          : pa::launch_tree<128>(tq, tk, tv, p, h->bf16, h->num_sms, s);
+  cudaError_t e = D == 64    ? pa::launch_tree<64>(tq, tk, tv, p, h->bf16, h->num_sms, s)
+                  : D == 128 ? pa::launch_tree<128>(tq, tk, tv, p, h->bf16, h->num_sms, s)
+                             : pa::launch_tree<256>(tq, tk, tv, p, h->bf16, h->num_sms, s);
   if (e != cudaSuccess) return tree_cuda_fail(h, e, "tree attention launch");
   return PA_OK;
 }

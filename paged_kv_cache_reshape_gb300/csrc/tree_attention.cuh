@@ -27,6 +27,11 @@
 // N 128 columns, O = head_size columns), P over S as 16-bit pairs, read from
 // there by the P V product.
 //
+// head_size 256: two O would not fit in tensor memory and 128-key tiles not in
+// the ring, so a unit has one row tile, key tiles are 64 keys, and one stream
+// (warpgroup 0) works through them with S double-buffered; the K/V bytes of a
+// tile still cover its softmax.
+//
 // Few rows (head_size 64, at most 64 or 32): the row tile holds every row 2 or
 // 4 times (REP), each replica takes the softmax of its own half or quarter of
 // a tile's keys (its P is zero at the others), and the replicas' O, m and l
@@ -60,7 +65,6 @@ constexpr int kControlWarp0 = 8;
 // Registers per thread after the split (launch: 168 each).
 constexpr int kRegSoftmax = 208, kRegControl = 80;
 static_assert(2 * kRegSoftmax + kRegControl <= 3 * 168, "register split");
-constexpr int kKeys = 128;   // keys per K/V tile
 constexpr int kRows = 128;   // rows per row tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyRescale = 8.f;  // log2 of the largest P value tolerated before rescaling
@@ -78,6 +82,8 @@ constexpr int kMinRange = 2;  // a line of less than twice this stays whole
 
 template <int D>
 struct TreeCfg {
+  static constexpr bool kOneO = D == 256;          // one stream
+  static constexpr int kKeys = kOneO ? 64 : 128;   // keys per K/V tile
   static constexpr int kChunks = D / 64;
   static constexpr int kQTileBytes = kRows * D * 2;  // [chunk][row][128 B]
   static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V tile [key / 8][chunk][key % 8][128 B]
@@ -92,7 +98,7 @@ struct TreeCfg {
     return rep > 1 ? 2 * kRows * kJoinChannels * 4 + 2 * kRows * 8 : 0;
   }
   static __host__ __device__ constexpr int s_col(int X) { return X * kKeys; }
-  static __host__ __device__ constexpr int o_col(int X) { return 2 * kKeys + X * D; }
+  static __host__ __device__ constexpr int o_col(int X) { return 2 * kKeys + (kOneO ? 0 : X * D); }
   static constexpr int kTmemCols = 512;
   static __host__ __device__ constexpr int smem_bytes(int q_tiles, int rep) {
     return q_tiles * kQTileBytes + slots(q_tiles, rep) * kSlotBytes + kCtrlBytes + join_bytes(rep);
@@ -124,6 +130,7 @@ struct Ctrl {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t pv_done;                   // one stream: after every PV
   uint64_t info_full[kInfoRing], info_empty[kInfoRing];
   uint64_t xchg_full, xchg_done, join[2];
   uint64_t drain;
@@ -154,6 +161,7 @@ struct SeqWork {
   int len;       // their length in the line
 };
 
+template <int kKeys>
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bits) {
   SeqWork s;
   s.t0 = p.cum[b];
@@ -173,7 +181,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bit
   } else if (s.n > 0) {
     s.lo = p.window >= 1 ? (max(0, s.past + 1 - p.window) & ~(kKeys - 1)) : 0;
     s.nt = (s.past + s.n - s.lo + kKeys - 1) / kKeys;
-    s.pairs = (((s.n - 1) * p.inv_pair) >> 20) + 1;  // ceil(n / (2 tile_tokens))
+    s.pairs = (((s.n - 1) * p.inv_unit) >> 20) + 1;  // ceil(n / unit_tokens)
     s.len = (s.nt + kUnitCost) * s.pairs;
   }
   return s;
@@ -224,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D>;
+  constexpr int kKeys = C::kKeys;
   static_assert(REP == 1 || D == 64, "replicated rows");
   const int S = C::slots(p.q_tiles, REP);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -249,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->xchg_full, 8);
       mbar_init(&ctl->xchg_done, 8);
       mbar_init(&ctl->drain, 1);
+      mbar_init(&ctl->pv_done, 1);
       ctl->abort = 0;
     }
     if (lane < kMaskRing) {
@@ -288,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      long long len = b < p.batch ? seq_work(p, b, bits).len : 0;
+      long long len = b < p.batch ? seq_work<kKeys>(p, b, bits).len : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) len += __shfl_xor_sync(0xffffffffu, len, o);
       // (no sum over a line of at most 2^31 - 1 wraps; a longer one is refused below)
@@ -330,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_window = [&](int& bits) {
         const int b = 32 * group + lane;
         mine = SeqWork{};
-        if (b < p.batch) mine = seq_work(p, b, bits);
+        if (b < p.batch) mine = seq_work<kKeys>(p, b, bits);
         seq_end = mine.len;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -403,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           f.b = 32 * group + src;
           if (lane == 0) prefetch_l1(p.block_table + (size_t)f.b * p.MB + ((s.lo + tile0 * kKeys) >> p.log_bs));
           f.k = chunk % p.Hk;
-          f.t0 = s.t0 + u * 2 * p.tile_tokens;
-          f.ntok = min(2 * p.tile_tokens, s.n - u * 2 * p.tile_tokens);
+          f.t0 = s.t0 + u * p.unit_tokens;
+          f.ntok = min(p.unit_tokens, s.n - u * p.unit_tokens);
           f.two = f.ntok > p.tile_tokens;
           f.seq_t0 = s.t0;
           f.n = s.n;
@@ -561,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and a wait on S(j + 2) covers PV(j).  First uses of tiles: with two
       // row tiles K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 K3 ... (the ring's
       // order, so that a slot is free as soon as it is the next to be filled).
+      constexpr int kFirstJobs = C::kOneO ? 1 : 2;  // jobs whose PV is the first into its O
       constexpr uint32_t idesc_s = umma_idesc_f16(kRows, kKeys, 0, 0, BF ? 1 : 0);
       constexpr uint32_t idesc_o = umma_idesc_f16(kRows, D, 0, 1, BF ? 1 : 0);
       const uint64_t desc_q = smem_desc_sw128(0, 16, 1024);                // K-major Q, + (address >> 4)
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= 2) {  // O_X += P_X V of job j - 2
             // its P; the segment's first PV of the stream overwrites O_X, which the last segment has read
             ok = wait_bar(&ctl->p_full[X], (pcnt >> X) & 1) &&
-                 (j >= 4 || tt == 0 || wait_bar(&ctl->o_free[X], (tt - 1) & 1));
+                 (j >= kFirstJobs + 2 || tt == 0 || wait_bar(&ctl->o_free[X], (tt - 1) & 1));
             if (!ok) break;
             pcnt ^= 1u << X;
             if (!two || X == 0) {
@@ -599,10 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b0 = desc_v + ((kv_addr + v_slot * C::kSlotBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_f16_ts(tmem + C::o_col(0) + X * D, tmem + X * kKeys + kk * 8, b0 + ((kk * 2 * C::kGroupBytes) >> 4), idesc_o,
-                          (j > 3 || kk > 0) ? 1u : 0u);
+              umma_f16_ts(tmem + C::o_col(0) + (C::kOneO ? 0 : X * D), tmem + X * kKeys + kk * 8,
+                          b0 + ((kk * 2 * C::kGroupBytes) >> 4), idesc_o, (j >= kFirstJobs + 2 || kk > 0) ? 1u : 0u);
             if (!two || X == 1) umma_commit(&ctl->empty[v_slot]);
-            if (j >= jobs) umma_commit(&ctl->o_done[X]);
+            if constexpr (C::kOneO) {
+              umma_commit(&ctl->pv_done);
+              if (j == jobs + 1) umma_commit(&ctl->o_done[0]);
+            } else {
+              if (j >= jobs) umma_commit(&ctl->o_done[X]);
+            }
           }
           if (j < jobs) {  // S_X = Q K^T of job j
             if (j == 0 && !(ok = wait_bar(&ctl->q_full, tt & 1))) break;
@@ -646,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float mul = GEN && (p.softcap > 0.f || p.slopes) ? 1.f : p.scale * kLog2e;
     uint32_t g = 0, scnt = 0, ocnt[2] = {0, 0};
+    uint32_t pvs = 0;  // one stream: PVs of earlier segments
     RingPos ring;  // of the segment's first load
     float x[COLS < 64 ? 64 : COLS];
     uint32_t joins = 0;  // phase of join[X]
@@ -675,7 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;  // no row admits a key below
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int i = two ? 0 : X; i < nt; i += two ? 1 : 2) {
+      // a stream's tiles: all of them (two row tiles), every other one, or, as the one stream, all
+      for (int i = C::kOneO ? X * nt : (two ? 0 : X); i < nt; i += C::kOneO || two ? 1 : 2) {
+        const int buf = C::kOneO ? i & 1 : X;  // S and P columns
         const uint32_t tile = g + i;
         const int key0 = sg.key0 + i * kKeys;
         // (published before the tile's K load: read before the wait for S,
@@ -750,16 +769,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!tree_wait(&ctl->s_full[X], scnt & 1, abort, 9)) {
+        if (!tree_wait(&ctl->s_full[buf], (C::kOneO ? scnt >> buf : scnt) & 1, abort, 9)) {
           ok = false;
           break;
         }
-        const bool first = i == (two ? 0 : X);
-        ++scnt;
+        const bool first = i == (two || C::kOneO ? 0 : X);
+        if constexpr (C::kOneO) scnt ^= 1u << buf;  // (a parity per buffer)
+        else ++scnt;
         tc_fence_after();
         if (warp_ok) {
 #pragma unroll
-          for (int c = 0; c < COLS; c += 32) tmem_ld32(lane_addr + C::s_col(X) + cb + c, x + c);
+          for (int c = 0; c < COLS; c += 32) tmem_ld32(lane_addr + C::s_col(buf) + cb + c, x + c);
           tmem_ld_wait();
           if constexpr (GEN) {
             if (p.softcap > 0.f) {
@@ -802,13 +822,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[q] = pack2<BF>(e0, e1);
             }
             // P -> TMEM over S: keys h..h+31 as 16 columns of 16-bit pairs
-            tmem_st16(lane_addr + C::s_col(X) + (cb + h) / 2, pk);
+            tmem_st16(lane_addr + C::s_col(buf) + (cb + h) / 2, pk);
           }
           if constexpr (REP > 1) {  // ... and zeros at the other replicas' keys
             const uint32_t zero[16] = {};
 #pragma unroll
             for (int h = 0; h < kKeys; h += 32)
-              if (h < cb || h >= cb + COLS) tmem_st16(lane_addr + C::s_col(X) + h / 2, zero);
+              if (h < cb || h >= cb + COLS) tmem_st16(lane_addr + C::s_col(buf) + h / 2, zero);
+          }
+          if constexpr (C::kOneO) {
+            // S(i) was issued before PV(i - 1): O is rescaled, and P(i) handed
+            // over, only once that has completed.
+            if (!first && !tree_wait(&ctl->pv_done, (pvs + i - 1) & 1, abort, 15)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
           }
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
             float o[32];
@@ -877,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[X]);
+        if (lane == 0) mbar_arrive(&ctl->p_full[buf]);
       }
       if (!ok) break;
 
@@ -913,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool keep_bad = any_bad != 0;  // read again after the stores: released there
       if (lane == 0 && !keep_bad) mbar_arrive(&ctl->xchg_done);
       const int jobs = two ? 2 * nt : nt;
-      bool have[2] = {true, jobs >= 2};
+      bool have[2] = {true, !C::kOneO && jobs >= 2};
       for (int Y = 0; Y < 2 && ok; ++Y) {
         if (!have[Y]) continue;
         if ((!two || Y == X) &&
@@ -1049,6 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int turn = ring.slot + 2 * nt;
       ring.phase ^= (turn / S) & 1;
       ring.slot = turn % S;
+      pvs += nt;
       if (lane == 0) mbar_arrive(&ctl->info_empty[slot]);
       g += nt;
     }
@@ -1161,10 +1191,10 @@ template <int D, bool BF, bool GEN, int REP>
 cudaError_t configure() {
   using C = TreeCfg<D>;
   static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
-  constexpr int kQTiles = REP > 1 ? 1 : 2;
+  constexpr int kQTiles = REP > 1 || C::kOneO ? 1 : 2;
   static_assert(C::smem_bytes(1, REP) <= kSmemLimit && C::smem_bytes(kQTiles, REP) <= kSmemLimit, "shared memory");
   static_assert(C::slots(kQTiles, REP) >= 4 && kMaxSlots / 2 + 3 <= kMaskRing, "K/V ring");
-  static_assert(2 * kKeys + 2 * D <= C::kTmemCols, "tensor memory");
+  static_assert(2 * C::kKeys + (C::kOneO ? 1 : 2) * D <= C::kTmemCols, "tensor memory");
   return cudaFuncSetAttribute(tree_kernel<D, BF, GEN, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               std::max(C::smem_bytes(1, REP), C::smem_bytes(kQTiles, REP)));
 }

@@ -81,6 +81,23 @@ CASES = {
                                 unmap=[(0, 0), (0, 1)]),
     "padding_rows": dict(past=[30, 20], n=[2, 3], H=4, Hk=2, D=64, bs=16, pad=9),
     "own_scale": dict(past=[60], n=[4], H=4, Hk=2, D=128, bs=16, scale=0.3),
+    "d256_one_token": dict(past=[0, 63, 64], n=[1, 1, 1], H=2, Hk=1, D=256, bs=16),
+    "d256_rows_over_tiles": dict(past=[130, 7], n=[70, 33], H=8, Hk=2, D=256, bs=32, dtype=BF16),
+    "d256_everything": dict(past=[700, 3, 129], n=[12, 20, 64], H=8, Hk=2, D=256, bs=64, softcap=8.0, window=250,
+                            slopes=True, sink=True),
+    "d256_long_axis": dict(past=[5000], n=[9], H=2, Hk=1, D=256, bs=128, dtype=BF16),
+    "d256_unmapped": dict(past=[200, 64], n=[10, 5], H=4, Hk=2, D=256, bs=16, unmap=[(0, 0), (0, 5), (1, 1)]),
+    "d64_long_axis_32_rows": dict(past=[7001], n=[8], H=4, Hk=1, D=64, bs=16),
+    "d64_long_axis_64_rows": dict(past=[6003, 100], n=[16, 9], H=8, Hk=2, D=64, bs=32, dtype=BF16, sink=True),
+    "d64_everything_32_rows": dict(past=[700, 3, 129], n=[5, 7, 8], H=8, Hk=2, D=64, bs=32, softcap=8.0, window=250,
+                                   slopes=True, sink=True, dtype=BF16),
+    "d64_everything_64_rows": dict(past=[900, 0, 127], n=[12, 16, 1], H=8, Hk=2, D=64, bs=16, softcap=8.0,
+                                   window=200, slopes=True, sink=True, mask="random"),
+    "long_axis_two_tiles": dict(past=[6000], n=[60], H=4, Hk=1, D=128, bs=64),
+    "one_head_of_many_pieces": dict(past=[20000], n=[3], H=1, Hk=1, D=128, bs=128),
+    "groups_of_128": dict(past=[100], n=[3], H=128, Hk=1, D=64, bs=16),
+    "groups_of_100": dict(past=[300], n=[2], H=100, Hk=1, D=128, bs=16, dtype=BF16),
+    "heads_beyond_the_sms": dict(past=[20, 0], n=[2, 1], H=200, Hk=200, D=64, bs=16),
     "many_sequences": dict(past=[(37 * i) % 90 for i in range(600)], n=[i % 3 for i in range(600)], H=2, Hk=1, D=64,
                            bs=16),
 }
@@ -91,25 +108,26 @@ def test_attention(name):
     check_attention(tree_ref.make_case(**CASES[name], seed=sum(map(ord, name))))
 
 
+@pytest.mark.parametrize("D,n", [(128, [40, 9]), (128, [70, 9]), (64, [14, 6]), (64, [30, 9]), (256, [40, 9])])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_masked_keys_never_reach_a_row(dtype, bad):
+def test_masked_keys_never_reach_a_row(dtype, bad, D, n):
     """Draft tokens whose K and V overflowed: the rows that do not admit them are as if they were not there; the
     rows that do are not finite."""
-    c = tree_ref.make_case([130, 0], [40, 9], 4, 2, 128, 16, dtype=dtype, seed=5)
+    c = tree_ref.make_case([130, 0], n, 4, 2, D, 16, dtype=dtype, seed=5)
     clean, _ = tree_ref.attention(c)
-    victims = {0: [6, 17, 39], 1: [4]}
+    victims = {0: [6, 11, n[0] - 1], 1: [4]}
     touched = torch.zeros(c["T"], dtype=torch.bool)
     for b, nodes in victims.items():
         for i in nodes:
             p = c["past"][b] + i
             slot = int(c["table"][b, p // c["bs"]]) * c["bs"] + p % c["bs"]
-            c["key_cache"].view(-1, 2, 128)[slot, :, 3] = bad
-            c["value_cache"].view(-1, 2, 128)[slot, :, 5] = bad
+            c["key_cache"].view(-1, 2, D)[slot, :, 3] = bad
+            c["value_cache"].view(-1, 2, D)[slot, :, 5] = bad
             rows = slice(int(c["cum"][b]), int(c["cum"][b + 1]))
             touched[rows] |= c["rows"][rows, i]
     _, out = attend(c)
-    got = out.double().cpu().view(c["T"], 4, 128)
+    got = out.double().cpu().view(c["T"], 4, D)
     assert touched.any() and not touched.all()
     u = tree_ref.HALF_STEP[dtype]
     # (the bound of the clean step: weights and values of these rows are untouched)
@@ -118,7 +136,7 @@ def test_masked_keys_never_reach_a_row(dtype, bad):
             p = c["past"][b] + i
             slot = int(c["table"][b, p // c["bs"]]) * c["bs"] + p % c["bs"]
             for name in ("key_cache", "value_cache"):
-                c[name].view(-1, 2, 128)[slot] = 0
+                c[name].view(-1, 2, D)[slot] = 0
     ref, tol = tree_ref.attention(c)
     keep = ~touched
     assert ((got[keep] - ref[keep]).abs() <= tol[keep]).all()
@@ -347,7 +365,7 @@ def write_case(c, R, off=0, inter=0, packed=False, seed=1):
 
 
 @pytest.mark.parametrize("packed", [False, True])
-@pytest.mark.parametrize("name", ["empty_context_tree", "sequences_without_tokens", "unmapped_pages", "padding_rows",
+@pytest.mark.parametrize("name", ["d256_unmapped", "empty_context_tree", "sequences_without_tokens", "unmapped_pages", "padding_rows",
                                   "many_rows", "many_sequences", "longest_draft"])
 def test_tree_write(name, packed):
     c = tree_ref.make_case(**CASES[name], seed=2)
@@ -438,7 +456,7 @@ def commit(c, paths, layers=3, width=None, op=None, past=None, count=None, table
     return err, pools.view(flat), dev.cpu().view(flat), new.cpu()
 
 
-@pytest.mark.parametrize("D,Hk,bs,dtype,layers", [(64, 1, 16, F16, 1), (128, 8, 16, BF16, 3), (128, 2, 64, F16, 130),
+@pytest.mark.parametrize("D,Hk,bs,dtype,layers", [(64, 1, 16, F16, 1), (256, 2, 32, F16, 2), (128, 8, 16, BF16, 3), (128, 2, 64, F16, 130),
                                                   (64, 5, 32, BF16, 7)])
 def test_commit(D, Hk, bs, dtype, layers):
     c = tree_ref.make_case([0, 37, 14, 5, 300, 2], [1, 40, 256, 9, 3, 20], Hk, Hk, D, bs, dtype=dtype, seed=1)

@@ -121,7 +121,8 @@ def cfg(**over):
 
 @pytest.mark.parametrize("over,draft,status,word", [
     (dict(num_heads=30), 8, pa.PA_INVALID_ARGUMENT, "num_heads"), (dict(), 0, pa.PA_INVALID_ARGUMENT, "max_draft"),
-    (dict(), 257, pa.PA_INVALID_ARGUMENT, "max_draft"), (dict(head_size=256), 8, pa.PA_NOT_SUPPORTED, "head_size"),
+    (dict(), 257, pa.PA_INVALID_ARGUMENT, "max_draft"), (dict(head_size=96), 8, pa.PA_NOT_SUPPORTED, "head_size"),
+    (dict(num_heads=8192), 8, pa.PA_NOT_SUPPORTED, "num_heads"),
     (dict(cache_dtype=pa.PA_CACHE_INT8, k_quant_type=1, v_quant_type=1), 8, pa.PA_NOT_SUPPORTED, "cache_dtype"),
     (dict(packed_qkv=1), 8, pa.PA_NOT_SUPPORTED, "packed_qkv"), (dict(qk_norm=1), 8, pa.PA_NOT_SUPPORTED, "qk_norm"),
     (dict(block_size=8), 8, pa.PA_INVALID_ARGUMENT, "block_size"),
