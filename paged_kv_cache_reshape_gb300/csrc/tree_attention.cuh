@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && cut.rows > 0) {  // units in two pieces from the front, in more from the back
           const int many = cut.more > 1, at = atomicAdd(&p.counters->n_cuts[many], 1);
-          p.cuts[many ? p.n_ranges * p.Hk - 1 - at : at] = cut;
+          if (at < p.n_ranges * p.Hk) p.cuts[many ? p.n_ranges * p.Hk - 1 - at : at] = cut;
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok || !f.live) break;

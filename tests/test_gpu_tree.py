@@ -567,3 +567,156 @@ def test_a_speculative_step_equals_plain_decoding(dtype):
     both = tol.view(c["T"], -1)[rows.cpu()] * 2
     assert ((out2.double().cpu() - out[rows].double().cpu()).abs() <= both).all()
     assert op.device_error() == 0
+
+
+# ---------------------------------------------------------------- how the calls are made
+
+
+def test_pools_beyond_32_bits():
+    """Pools of more than 2^32 elements whose used blocks lie at their end."""
+    H, Hk, D, bs, past, n = 8, 8, 128, 128, [200, 30], [4, 6]
+    c = tree_ref.make_case(past, n, H, Hk, D, bs, seed=21)
+    NB = 2 ** 32 // (bs * Hk * D) + 9
+    far = NB - c["NB"]
+    kc, vc = (torch.empty(NB, bs, Hk, D, dtype=F16, device="cuda") for _ in range(2))
+    kc[far:], vc[far:] = c["key_cache"].cuda(), c["value_cache"].cuda()
+    cfg = pa.make_config(H, Hk, D, bs, NB, c["MB"], 2, c["T"])
+    op = pa.PagedTree(cfg, c["max_draft"])
+    table = torch.where(c["table"] >= 0, c["table"] + far, c["table"]).cuda()
+    d = {k: c[k].cuda() for k in ("query", "cum", "past_t", "pos", "mask")}
+    out = torch.empty(c["T"], H * D, dtype=F16, device="cuda")
+    op.attention(d["query"], kc, vc, table, d["cum"], d["past_t"], 2, c["T"], out, positions=d["pos"],
+                 tree_mask=d["mask"])
+    ref, tol = tree_ref.attention(c)
+    assert ((out.double().cpu().view(c["T"], H, D) - ref).abs() <= tol).all()
+    q, k, v, steps, rc = write_case(c, D)
+    qo, before_v = torch.empty_like(q), vc[far:].clone()
+    op.write(rc, pa.rotary_steps_tensor(steps), d["pos"], q, k, v, qo, kc, vc, table, d["cum"], d["past_t"], 2, c["T"])
+    for b in range(2):
+        for j in range(n[b]):
+            p = past[b] + j
+            slot = int(c["table"][b, p // bs]) * bs + p % bs
+            before_v.view(-1, Hk * D)[slot] = v[int(c["cum"][b]) + j]
+    assert torch.equal(vc[far:].view(torch.int16), before_v.view(torch.int16))  # (bits: unused slots are NaN)
+    acc = torch.tensor([[1, 3], [2, 5]], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    op.commit(pa.layer_pools([kc], [vc]), table, d["past_t"], acc, cnt, 2)
+    for b, path in enumerate(acc.tolist()):
+        for i, a in enumerate(path):
+            to, of = (int(c["table"][b, p // bs]) * bs + p % bs for p in (past[b] + i, past[b] + a))
+            assert torch.equal(vc[far:].view(-1, Hk * D)[to], before_v.view(-1, Hk * D)[of])
+    assert op.device_error() == 0
+
+
+def test_two_handles_at_once_on_two_streams():
+    """A handle per stream: steps that overlap on the GPU give what they give alone."""
+    cs = [tree_ref.make_case([3000, 900], [20, 8], 8, 2, 128, 16, dtype=BF16, seed=31),
+          tree_ref.make_case([500, 2500, 7], [5, 7, 8], 4, 1, 64, 32, seed=32)]
+    ops = [handle(c) for c in cs]
+    dev = [{k: cuda(c[k]) for k in ("query", "key_cache", "value_cache", "table", "cum", "past_t", "positions", "mask")}
+           for c in cs]
+    alone = [attend(c, op)[1] for c, op in zip(cs, ops)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [[torch.empty_like(a) for _ in range(20)] for a in alone]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, op, d, s, o in zip(cs, ops, dev, streams, outs):
+            op.attention(d["query"], d["key_cache"], d["value_cache"], d["table"], d["cum"], d["past_t"], c["B"],
+                         c["T"], o[i], positions=d["positions"], tree_mask=d["mask"], stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert all(torch.equal(a, x) for x in o)
+    assert all(op.device_error() == 0 for op in ops)
+
+
+def test_a_captured_step_replays():
+    """write, attention and commit in one graph, replayed on new tokens."""
+    c = tree_ref.make_case([300, 45], [9, 12], 4, 2, 128, 16, seed=41)
+    op = handle(c)
+    q, k, v, steps, rc = write_case(c, 128)
+    st = pa.rotary_steps_tensor(steps)
+    d = {n: c[n].cuda() for n in ("table", "cum", "past_t", "pos", "mask")}
+    kc, vc = c["key_cache"].cuda(), c["value_cache"].cuda()
+    qr, out, new = torch.empty_like(q), torch.empty_like(q), torch.zeros(2, dtype=torch.int32, device="cuda")
+    acc = torch.tensor([[0, 2, 5], [0, 1, 0]], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([3, 2], dtype=torch.int32, device="cuda")
+    layers = pa.layer_pools([kc], [vc])
+
+    def step(s):
+        op.write(rc, st, d["pos"], q, k, v, qr, kc, vc, d["table"], d["cum"], d["past_t"], 2, c["T"], stream=s)
+        op.attention(qr, kc, vc, d["table"], d["cum"], d["past_t"], 2, c["T"], out, positions=d["pos"],
+                     tree_mask=d["mask"], stream=s)
+        op.commit(layers, d["table"], d["past_t"], acc, cnt, 2, new_past=new, stream=s)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(s.cuda_stream)
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda").to(F16))
+        kc.copy_(c["key_cache"].cuda())
+        vc.copy_(c["value_cache"].cuda())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (qr, out, kc, vc, new)]
+        kc.copy_(c["key_cache"].cuda())
+        vc.copy_(c["value_cache"].cuda())
+        step(None)
+        torch.cuda.synchronize()
+        for a, b in zip(got, (qr, out, kc, vc, new)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert op.device_error() == 0
+
+
+def test_write_in_place_and_single_rows():
+    c = tree_ref.make_case([33], [1], 4, 2, 64, 16, seed=51)
+    op = handle(c)
+    q, k, v, steps, rc = write_case(c, 64, packed=True)
+    st = pa.rotary_steps_tensor(steps)
+    kc, vc = c["key_cache"].cuda(), c["value_cache"].cuda()
+    args = (kc, vc, c["table"].cuda(), c["cum"].cuda(), c["past_t"].cuda(), 1, 1)
+    out = torch.empty(1, 256, dtype=F16, device="cuda")
+    op.write(rc, st, c["pos"].cuda(), q, k, v, out, *args)
+    q2 = q.clone()
+    op.write(rc, st, c["pos"].cuda(), q2, k, v, q2, *args)
+    assert torch.equal(out, q2) and op.device_error() == 0
+
+
+def test_refusals_of_calls():
+    c = tree_ref.make_case([33], [3], 4, 2, 64, 16, seed=52)
+    op = handle(c)
+    q, k, v, steps, rc = write_case(c, 64)
+    st = pa.rotary_steps_tensor(steps)
+    d = {n: c[n].cuda() for n in ("table", "cum", "past_t", "pos")}
+    kc, vc = c["key_cache"].cuda(), c["value_cache"].cuda()
+    out = torch.empty_like(q)
+
+    def refused(word, f, *a, **kw):
+        with pytest.raises(pa.PAError) as e:
+            f(*a, **kw)
+        assert e.value.status == pa.PA_INVALID_ARGUMENT and word in e.value.message, e.value
+
+    w = lambda **o: [o.get("rc", rc), st, d["pos"], o.get("q", q), k, v, o.get("out", out), o.get("kc", kc),  # noqa: E731
+                     o.get("vc", vc), d["table"], d["cum"], d["past_t"], o.get("batch", 1), o.get("T", 3)]
+    refused("head_size and dtype", op.write, *w(rc=pa.make_rotary_config(128)))
+    refused("head_size and dtype", op.write, *w(rc=pa.make_rotary_config(64, dtype=pa.PA_ROTARY_BF16)))
+    refused("batch", op.write, *w(batch=2))
+    refused("token_count", op.write, *w(T=4))
+    refused("distinct", op.write, *w(vc=kc))
+    refused("query_out", op.write, *w(out=k))
+    refused("pools", op.write, *w(out=kc.view(-1, 256)[:3]))
+    refused("2-D", op.write, *w(q=q.view(3, 4, 64)))
+    a = lambda **o: [o.get("q", q), o.get("kc", kc), vc, d["table"], d["cum"], d["past_t"], o.get("batch", 1),  # noqa: E731
+                     o.get("T", 3), o.get("out", out)]
+    refused("output", op.attention, *a(out=q))
+    refused("output", op.attention, *a(out=kc.view(-1, 256)[:3]))
+    refused("batch", op.attention, *a(batch=0))
+    refused("token_count", op.attention, *a(T=4))
+    refused("aligned", op.attention, *a(out=torch.empty(3 * 256 + 1, dtype=F16, device="cuda")[1:]))
+    refused("distinct", op.attention, *a(kc=vc))
+    op.attention(*a(T=0))
+    op.write(*w(T=0))
+    assert op.device_error() == 0
