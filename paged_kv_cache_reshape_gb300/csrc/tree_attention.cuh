@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cb = r / R * COLS;        // first of the tile's keys that this replica takes
     const int rj = row / p.G;           // the row's token within the tile
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float mul = GEN && (p.softcap > 0.f || p.slopes) ? 1.f : p.scale * kLog2e;
+    const float mul = GEN && p.softcap > 0.f ? 1.f : p.scale * kLog2e;  // of the scores, to log2 units
     uint32_t g = 0, scnt = 0, ocnt[2] = {0, 0};
     uint32_t pvs = 0;  // one stream: PVs of earlier segments
     RingPos ring;  // of the segment's first load
@@ -683,11 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = sg.t0 + (row_ok ? jt : 0);
       const int j_seq = t - sg.seq_t0;  // its draft index
       int qpos = 0, lo_row = 0;
-      float slope2 = 0.f;
+      float slope = 0.f;  // of the distance bias, in units of 1 / mul
       if constexpr (GEN) {
         qpos = p.positions ? p.positions[t] : past + j_seq;
         if (p.window >= 1) lo_row = max(max(qpos, past) - p.window + 1, 0);
-        if (p.slopes && row_ok) slope2 = p.slopes[sg.k * p.G + (row - rj * p.G)] * kLog2e;
+        if (p.slopes && row_ok) slope = p.slopes[sg.k * p.G + (row - rj * p.G)] * (kLog2e / mul);
       }
       const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;  // no row admits a key below
       float m_ref = -INFINITY, l = 0.f;
@@ -706,15 +706,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t pmask = ctl->kv_mask[tile % kMaskRing];
         // A tile that is not admitted as a whole: one bit per key of this row
         // (made before the wait for S).
-        const bool partial = key0 + kKeys > past || pmask != 0 || __any_sync(0xffffffffu, key0 < lo_row || !row_ok);
+        // (Lanes without a row compute on whatever Q's buffer holds there: no
+        // other row sees it.)
+        const bool partial = key0 + kKeys > past || pmask != 0 || __any_sync(0xffffffffu, row_ok && key0 < lo_row);
         const bool drafts = key0 + kKeys > past;
         constexpr int NW = COLS / 32;
         uint32_t w[NW];
-        float kpf[NW];  // GEN: lane e, entry q: position of key cb + 32 q + e, less past
+        float ahead[NW];  // GEN: lane e, entry q: position of key cb + 32 q + e, less its slot
 #pragma unroll
         for (int q = 0; q < NW; ++q) {
           w[q] = ~0u;
-          if constexpr (GEN) kpf[q] = (float)(key0 + cb + 32 * q + lane - past);
+          ahead[q] = 0.f;
         }
         if (partial && warp_ok) {
           int kp[NW];
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int q = 0; q < NW; ++q) {
                 const int d = key0 + cb + 32 * q + lane - past;
                 kp[q] = d >= 0 && d < n ? p.positions[sg.seq_t0 + d] : past + d;
-                kpf[q] = (float)(kp[q] - past);
+                ahead[q] = (float)(kp[q] - (past + d));
               }
             }
           }
@@ -747,8 +749,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.window >= 1) {
                   uint32_t in = 0;
                   if (p.positions) {
+                    // (as a rule no row's window leaves a draft token out)
+                    const int d = d0 + lane, far = __reduce_min_sync(0xffffffffu, d >= 0 && d < n ? kp[q] : 0x7fffffff);
+                    if (__any_sync(0xffffffffu, far < lo_row)) {
 #pragma unroll 1
-                    for (int e = 0; e < 32; ++e) in |= (__shfl_sync(0xffffffffu, kp[q], e) >= lo_row ? 1u : 0u) << e;
+                      for (int e = 0; e < 32; ++e) in |= (__shfl_sync(0xffffffffu, kp[q], e) >= lo_row ? 1u : 0u) << e;
+                    } else {
+                      in = ~0u;
+                    }
                   } else {
                     in = bit_range(lo_row - k0, 32);
                   }
@@ -789,25 +797,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < COLS; ++c) x[c] = fmaf(-2.f * out, rcp(1.f + ex2(x[c] * in)), out);
             }
-            if (p.slopes) {
-              const float unit = p.softcap > 0.f ? 1.f : p.scale * kLog2e, base = slope2 * (float)(past - qpos);
+            // the bias's part that grows along the tile (`shift` holds the rest;
+            // without a bias the slope is 0)
 #pragma unroll
-              for (int c = 0; c < COLS; ++c)
-                x[c] = fmaf(x[c], unit, fmaf(slope2, __shfl_sync(0xffffffffu, kpf[c >> 5], c & 31), base));
-            }
+            for (int c = 0; c < COLS; ++c) x[c] = fmaf(slope, (float)c, x[c]);
           }
           if (partial) {
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) x[c] = ((w[c >> 5] >> (c & 31)) & 1) ? x[c] : -INFINITY;
+            for (int c = 0; c < COLS; ++c) {
+              // (draft tokens stand at positions of their own)
+              const float moved = GEN ? fmaf(slope, __shfl_sync(0xffffffffu, ahead[c >> 5], c & 31), x[c]) : x[c];
+              x[c] = ((w[c >> 5] >> (c & 31)) & 1) ? moved : -INFINITY;
+            }
           }
-          const float cand = max_tree<COLS>(x) * mul;
+          const float shift = GEN ? slope * (float)(key0 + cb - qpos) * mul : 0.f;
+          const float cand = fmaf(max_tree<COLS>(x), mul, shift);
           float alpha = 1.f;
           if (cand > m_ref + kLazyRescale || (m_ref == -INFINITY && cand != -INFINITY)) {
             alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - cand);
             m_ref = cand;
           }
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t mul2 = f2(mul, mul), neg_m2 = f2(-m_use, -m_use);
+          const uint64_t mul2 = f2(mul, mul), neg_m2 = f2(shift - m_use, shift - m_use);
           uint64_t sum2[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int h = 0; h < COLS; h += 32) {
