@@ -492,13 +492,14 @@ PA_API void pa_rotary_config_init(pa_rotary_config* rc);
  *   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a)
  * in fp32, rounded once to the type; the other channels are copied.
  * Row t of a tensor starts at t * stride elements (a multiple of 8, at least
- * heads * D; 0 => heads * D; one row has no stride), so slices of packed rows are taken and written
- * in place.  query_out == query with equal strides rotates in place; an
- * output that overlaps its input in any other way is refused, and so are
- * outputs that overlap each other or the other input.  Overlap is decided by
- * whole ranges of rows, save that two slices of one row layout (equal
- * strides, disjoint columns) do not overlap.  num_heads or kv_num_heads 0
- * leaves that tensor out (at most 4096 of each).  Runs on the current device; keeps nothing, so calls may overlap. */
+ * heads * D; 0 => heads * D; one row has no stride), so slices of packed rows
+ * are taken and written in place.  query_out == query with equal strides
+ * rotates in place; an output that overlaps its input in any other way is
+ * refused, and so are outputs that overlap each other or the other input.
+ * Overlap is decided by whole ranges of rows, save that two slices of one row
+ * layout (equal strides, disjoint columns) do not overlap.  num_heads or
+ * kv_num_heads 0 leaves that tensor out (at most 4096 of each).  Runs on the
+ * current device; keeps nothing, so calls may overlap. */
 PA_API pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int32_t* positions,
                            int token_count, int num_heads, const void* query, int64_t query_stride,
                            void* query_out, int64_t query_out_stride, int kv_num_heads, const void* key,
@@ -512,9 +513,10 @@ typedef struct pa_tree_handle_s* pa_tree_handle;
  * max_tokens, max_kv_len_bound and cache_dtype (PA_CACHE_FP16 or
  * PA_CACHE_BF16, the activations' type too).  Its rotary fields are not read
  * here (positions are explicit; pa_tree_write takes a pa_rotary_config).
- * PA_NOT_SUPPORTED: 8-bit caches, the latent
- * layout, packed_qkv, qk_norm, more than 4096 heads.  Allocates the workspace (split-KV partials,
- * error word) on the current device.
+ * PA_NOT_SUPPORTED: 8-bit caches, the latent layout, packed_qkv, qk_norm,
+ * more than 4096 heads.  Allocates the workspace (split-KV partials, error
+ * word) on the current device; other calls run there whatever is current.
+ * A batch of more than 2^31 key tiles is flagged (PA_DEVERR_KV_BOUND).
  * One handle's pa_tree_attention calls share that workspace: calls (and
  * replays of graphs captured from them) on one handle must not overlap on the
  * GPU; use a handle per stream.  pa_tree_write and pa_tree_commit do not use it. */
@@ -547,10 +549,12 @@ typedef struct {
  * (at position p; -1 pages are masked) and draft token i under the mask (at
  * positions[cum[b] + i]); with local_window_size W only keys at positions
  * > max(positions[t], past[b]) - W.  x = scale <q, k>, softcapped, plus the
- * bias; output = sum softmax(x) v, 0 when nothing is admitted.  A key that a
- * row does not admit never reaches that row, whatever its K and V hold
- * (window edges: V must be finite there).  query, output [T, H*D]; output
- * must not overlap the inputs.  P is rounded to the 16-bit type for the P*V
+ * bias (positions of a sequence's keys and rows within 2^31 of one another);
+ * output = sum softmax(x) v, 0 when nothing is admitted.  A key that a row
+ * does not admit never reaches that row, whatever its K and V hold (under a
+ * window this holds for rows at positions below past[b] + max_draft_tokens;
+ * a row further on needs finite V at its window's edge).  query, output
+ * [T, H*D]; output must not overlap the inputs.  P is rounded to the 16-bit type for the P*V
  * contraction; scores, sums and the output accumulate in fp32. */
 PA_API pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key_cache,
                                    const void* value_cache, const int32_t* block_table,

@@ -451,6 +451,17 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   const Rows kc{key_cache, 1, pool, pool}, vc{value_cache, 1, pool, pool};
   if (overlap(o, q) || overlap(o, kc) || overlap(o, vc))
     return tree_fail(h, PA_INVALID_ARGUMENT, "output must not overlap query or the pools");
+  struct { const void* p; long long bytes; const char* name; } reads[] = {
+      {x->positions, 4LL * token_count, "positions"},
+      {x->tree_mask, 4LL * token_count * h->words, "tree_mask"},
+      {x->distance_slopes, 4LL * H, "distance_slopes"},
+      {x->head_sink, 2LL * H, "head_sink"},
+      {block_table, 4LL * batch * c.max_blocks_per_seq, "block_table"},
+      {cum, 4LL * (batch + 1), "cumulative_sequence_lengths"},
+      {past, 4LL * batch, "past_sequence_lengths"}};
+  for (auto& r : reads)
+    if (r.p && overlap(o, Rows{r.p, 1, r.bytes, r.bytes}))
+      return tree_fail(h, PA_INVALID_ARGUMENT, "output must not overlap %s", r.name);
   OnDevice g(h->device);
   pa::TreeParams p{};
   p.value_cache = static_cast<const __half*>(value_cache);

@@ -42,8 +42,9 @@
 // draft tokens, a window's edge or an unmapped page builds one 128-bit mask
 // per row.  P is zero at masked keys, and 0 * inf would still be NaN in the
 // P V product, so V rows past the sequence are zeroed in shared memory, and
-// non-finite values in draft rows (which only some rows admit) are taken out
-// there and added to the rows that do admit them when O leaves tensor memory.
+// non-finite values in keys that only some rows admit (drafts, the context at
+// a window's edge) are taken out there and added to the rows that do admit
+// them when O leaves tensor memory.
 //
 // Roles (384 threads): warpgroups 0 and 1, softmax and epilogue of the two
 // streams (thread = row = TMEM lane); warps 8 and 11 K and V producers (TMA,
@@ -124,7 +125,9 @@ struct Segment {
 struct Ctrl {
   Segment seg[kInfoRing];
   float2 ml[2][kRows];                // per stream: running maximum and sum of the segment
-  uint32_t bad[2][2][kTreeMaxWords];  // per segment parity and stream: draft tokens with non-finite V
+  // Per segment parity: keys with non-finite V, first the draft tokens, then
+  // the context from the window's edge `lo_min` on.
+  uint32_t bad[2][2 * kTreeMaxWords];
   uint8_t kv_mask[kMaskRing];         // per K/V tile (tile number mod ring): its pages that are unmapped
   uint64_t mask_full[kMaskRing];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
@@ -219,10 +222,11 @@ template <bool BF>
 __device__ __forceinline__ bool nonfinite16(uint32_t h) {
   return BF ? (h & 0x7f80u) == 0x7f80u : (h & 0x7c00u) == 0x7c00u;
 }
-
-// Word of the segment's draft tokens with non-finite V that holds token i.
-__device__ __forceinline__ uint32_t bad_word(const Ctrl* ctl, int parity, int i) {
-  return ctl->bad[parity][0][i >> 5] | ctl->bad[parity][1][i >> 5];
+// The same for both halves of w, at bits 15 and 31: an exponent of all ones
+// carries into the sign's place.
+template <bool BF>
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
+  return (BF ? (w & 0x7f807f80u) + 0x00800080u : (w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
 // GEN: softcap, distance bias or a window (checked at run time); without it
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (threadIdx.x < 4 * kTreeMaxWords) ctl->bad[0][0][threadIdx.x] = 0;
+  if (threadIdx.x < 4 * kTreeMaxWords) ctl->bad[0][threadIdx.x] = 0;
   if (warp == kFetchWarp && lane == 0) prefetch_tmap(&tm_q);
   if (warp == kKWarp && lane == 0) prefetch_tmap(&tm_k);
   if (warp == kVWarp && lane == 0) prefetch_tmap(&tm_v);
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cb = r / R * COLS;        // first of the tile's keys that this replica takes
     const int rj = row / p.G;           // the row's token within the tile
     const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float mul = GEN && p.softcap > 0.f ? 1.f : p.scale * kLog2e;  // of the scores, to log2 units
+    const float mul = (GEN && p.softcap > 0.f ? p.softcap : p.scale) * kLog2e;  // of x, to log2 units
     uint32_t g = 0, scnt = 0, ocnt[2] = {0, 0};
     uint32_t pvs = 0;  // one stream: PVs of earlier segments
     RingPos ring;  // of the segment's first load
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the exchange of the last segment has been read by both streams
       if (tt > 0) {
         if (!tree_wait(&ctl->xchg_done, (tt - 1) & 1, abort, 7)) break;
-        if ((warp & 3) == 0 && lane < kTreeMaxWords) ctl->bad[(tt - 1) & 1][X][lane] = 0;
+        if (warp == 0 && lane < 2 * kTreeMaxWords) ctl->bad[(tt - 1) & 1][lane] = 0;
       }
       const int two = sg.two, nt = sg.nt, past = sg.past, n = sg.n;
       const int jt = (two ? X * p.tile_tokens : 0) + rj;  // the row's token within the unit
@@ -689,7 +693,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.window >= 1) lo_row = max(max(qpos, past) - p.window + 1, 0);
         if (p.slopes && row_ok) slope = p.slopes[sg.k * p.G + (row - rj * p.G)] * (kLog2e / mul);
       }
-      const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;  // no row admits a key below
+      // Zero V rows that no row admits by position, take non-finite values out of
+      // rows that only some admit: the drafts, and the context at the window's
+      // edge (once per tile: stream 0 when both use it).  Unmapped pages and
+      // pages behind the sequence are zero already.  Called before the wait for
+      // S, whose tensor work it then overlaps; by GEN after the softmax, because
+      // a window's first V tiles come later than their K (before: 128 sequences
+      // of 200..500 keys 62.2 -> 58.9 us; after: a window of 1000 72.2 -> 70.5).
+      auto mend_v = [&](int i, int key0) -> bool {
+        // no row admits a key below lo_min, and every row the context from lo_edge on
+        const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;
+        const int lo_edge = GEN && p.window >= 1 ? min(past - p.window + p.max_draft, past) : 0;
+        // the tile's V load, counted from the segment's first, in the ring's order
+        const int n_v = two ? 2 * i + 1 : (i == nt - 1 ? 2 * i + 1 : 2 * i + 2);
+        const int turn = ring.slot + n_v, sv = turn % S;
+        if (!tree_wait(&ctl->full[sv], ring.phase ^ ((turn / S) & 1), abort, 10)) return false;
+        uint8_t* vs = kv_s + sv * C::kSlotBytes;
+        const int page_rows = 1 << log_r;
+        const int k_lo = min(max(lo_min - key0, 0), kKeys);      // rows below: zero
+        const int k_draft = min(max(past - key0, 0), kKeys);     // draft rows from here on
+        const int k_edge = min(max(lo_edge - key0, 0), kKeys);   // (not above k_draft)
+        const int k_end = min(max(past + n - key0, 0), kKeys);   // rows from here on: zero
+        const int k_page = min((k_end + page_rows - 1) & ~(page_rows - 1), kKeys);  // ... up to here
+        constexpr int kVecs = C::kChunks * 8;  // 16-byte vectors of a row
+#pragma unroll 1
+        for (int idx = r; idx < (k_edge + k_page - k_draft) * kVecs; idx += kRows) {
+          int kr = idx / kVecs;
+          const int v8 = idx % kVecs;
+          if (kr >= k_edge) kr += k_draft - k_edge;
+          uint4* at = reinterpret_cast<uint4*>(vs + (kr >> 3) * C::kGroupBytes + (v8 >> 3) * 1024 + (kr & 7) * 128 +
+                                               (((v8 & 7) ^ (kr & 7)) << 4));
+          if (kr < k_lo || kr >= k_end) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          const uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (nonfinite_halves<BF>(w[0]) | nonfinite_halves<BF>(w[1]) | nonfinite_halves<BF>(w[2]) |
+              nonfinite_halves<BF>(w[3])) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] &= ~((nonfinite_halves<BF>(w[e]) >> 15) * 0xffffu);
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            const int bit = key0 + kr - (kr >= k_draft ? past : lo_min - kTreeMaxDraft);
+            atomicOr(&ctl->bad[tt & 1][bit >> 5], 1u << (bit & 31));
+          }
+        }
+        fence_proxy_async_smem();
+        return true;
+      };
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       // a stream's tiles: all of them (two row tiles), every other one, or, as the one stream, all
@@ -777,6 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        const bool mend = (drafts || (GEN && p.window >= 1 && key0 < past - p.window + p.max_draft)) && (!two || X == 0);
+        if (!GEN && mend && !mend_v(i, key0)) {
+          ok = false;
+          break;
+        }
         if (!tree_wait(&ctl->s_full[buf], (C::kOneO ? scnt >> buf : scnt) & 1, abort, 9)) {
           ok = false;
           break;
@@ -791,30 +847,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           if constexpr (GEN) {
             if (p.softcap > 0.f) {
-              // c tanh(y), y = S scale / c, in log2 units.  Where no |y| of the
-              // warp is above 0.7 (scores well below the cap, the usual case) by
-              // the polynomial y p(y^2) that meets tanh at the Chebyshev points
+              // x = tanh(y), y = S scale / c, in units of the cap c.  Where no |y| of
+              // the warp is above 0.7 (scores well below the cap, the usual case)
+              // by the polynomial y p(y^2) that meets tanh at the Chebyshev points
               // of y^2 in [0, 0.5] (off by 4.1e-7 relative), two columns per
-              // instruction and no exponential unit; otherwise
-              // c (1 - 2 / (1 + e^{2y})), whose approximate reciprocal is off by
-              // 2^-23 of a term below 2 c.
-              const float in = p.scale / p.softcap, out = p.softcap * kLog2e;
+              // instruction and no exponential unit; otherwise 1 - 2 / (1 + e^{2y}),
+              // whose approximate reciprocal is off by 2^-23 of a term below 2.
+              const float in = p.scale / p.softcap;
               float top = 0.f;
 #pragma unroll
               for (int c = 0; c < COLS; c += 2) top = max3(top, fabsf(x[c]), fabsf(x[c + 1]));
               if (__any_sync(0xffffffffu, row_ok && !(top * fabsf(in) <= 0.7f))) {
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) x[c] = fmaf(-2.f * out, rcp(1.f + ex2(x[c] * (2.f * kLog2e * in))), out);
+                for (int c = 0; c < COLS; ++c) x[c] = fmaf(-2.f, rcp(1.f + ex2(x[c] * (2.f * kLog2e * in))), 1.f);
               } else {
-                const uint64_t in2 = f2(in, in), c0 = f2(0.999999663f * out, 0.999999663f * out),
-                               c1 = f2(-0.333299451f * out, -0.333299451f * out),
-                               c2 = f2(0.132779678f * out, 0.132779678f * out),
-                               c3 = f2(-0.0507202948f * out, -0.0507202948f * out),
-                               c4 = f2(0.0136421223f * out, 0.0136421223f * out);
+                const uint64_t in2 = f2(in, in);
 #pragma unroll
                 for (int c = 0; c < COLS; c += 2) {
                   const uint64_t y = mul2(f2(x[c], x[c + 1]), in2), t = mul2(y, y);
-                  unf2(mul2(y, fma2(fma2(fma2(fma2(c4, t, c3), t, c2), t, c1), t, c0)), x[c], x[c + 1]);
+                  uint64_t a = f2(0.0136421223f, 0.0136421223f);
+                  a = fma2(a, t, f2(-0.0507202948f, -0.0507202948f));
+                  a = fma2(a, t, f2(0.132779678f, 0.132779678f));
+                  a = fma2(a, t, f2(-0.333299451f, -0.333299451f));
+                  a = fma2(a, t, f2(0.999999663f, 0.999999663f));
+                  unf2(mul2(y, a), x[c], x[c + 1]);
                 }
               }
             }
@@ -887,53 +943,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           unf2(add2(sum2[2], sum2[3]), s2, s3);
           l = l * alpha + ((s0 + s1) + (s2 + s3));
         }
-        // Zero V rows that no row admits by position, take non-finite values
-        // out of draft rows (once per tile: stream 0 when both use it).
-        // Unmapped pages and pages behind the sequence are zero already.
-        if ((key0 + kKeys > past || key0 < lo_min) && (!two || X == 0)) {
-          // the tile's V load, counted from the segment's first, in the ring's order
-          const int n_v = two ? 2 * i + 1 : (i == nt - 1 ? 2 * i + 1 : 2 * i + 2);
-          const int turn = ring.slot + n_v, sv = turn % S;
-          if (!tree_wait(&ctl->full[sv], ring.phase ^ ((turn / S) & 1), abort, 10)) {
-            ok = false;
-            break;
-          }
-          uint8_t* vs = kv_s + sv * C::kSlotBytes;
-          const int page_rows = 1 << log_r;
-          const int k_lo = min(max(lo_min - key0, 0), kKeys);                        // rows below: zero
-          const int k_draft = max(past - key0, 0);                                   // draft rows
-          const int k_end = max(past + n - key0, 0);                                 // rows from here on: zero
-          const int k_page = min((k_end + page_rows - 1) & ~(page_rows - 1), kKeys);  // ... up to here
-          constexpr int kVecs = C::kChunks * 8;  // 16-byte vectors of a row
-          auto vec_at = [&](int kr, int v) {
-            return reinterpret_cast<uint4*>(vs + (kr >> 3) * C::kGroupBytes + (v >> 3) * 1024 + (kr & 7) * 128 +
-                                            (((v & 7) ^ (kr & 7)) << 4));
-          };
-#pragma unroll 1
-          for (int idx = r; idx < k_lo * kVecs; idx += kRows) *vec_at(idx / kVecs, idx % kVecs) = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-          for (int idx = k_draft * kVecs + r; idx < k_page * kVecs; idx += kRows) {
-            const int kr = idx / kVecs;
-            uint4* at = vec_at(kr, idx % kVecs);
-            if (kr >= k_end) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (kr >= k_lo) {
-              const uint4 v = *at;
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              bool any = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (nonfinite16<BF>(w[e])) { w[e] &= 0xffff0000u; any = true; }
-                if (nonfinite16<BF>(w[e] >> 16)) { w[e] &= 0x0000ffffu; any = true; }
-              }
-              if (any) {
-                const int d = key0 + kr - past;
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
-                atomicOr(&ctl->bad[tt & 1][X][d >> 5], 1u << (d & 31));
-              }
-            }
-          }
-          fence_proxy_async_smem();
+        if (GEN && mend && !mend_v(i, key0)) {
+          ok = false;
+          break;
         }
         tmem_st_wait();
         tc_fence_before();
@@ -969,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      uint32_t any_bad = lane < kTreeMaxWords ? bad_word(ctl, tt & 1, 32 * lane) : 0u;
+      uint32_t any_bad = lane < 2 * kTreeMaxWords ? ctl->bad[tt & 1][lane] : 0u;
       any_bad = __any_sync(0xffffffffu, any_bad != 0);
       const bool keep_bad = any_bad != 0;  // read again after the stores: released there
       if (lane == 0 && !keep_bad) mbar_arrive(&ctl->xchg_done);
@@ -1085,13 +1097,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&ctl->o_free[1]);
       }
       if (any_bad && row_ok && r < R) {
-        // Draft keys with non-finite V: added, element by element, to what
-        // has just been stored for the row if the row admits them.
+        // Keys with non-finite V: added, element by element, to what has just
+        // been stored for the row if the row admits them.
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          if (!((bad_word(ctl, tt & 1, i) >> (i & 31)) & 1) || !mask_bit(p, t, j_seq, i)) continue;
-          const int pos = past + i;
-          if (GEN && p.window >= 1 && (p.positions ? p.positions[sg.seq_t0 + i] : pos) < lo_row) continue;
+        for (int i = 0; i < 2 * kTreeMaxDraft; ++i) {
+          const uint32_t left = ctl->bad[tt & 1][i >> 5] >> (i & 31);
+          if (left == 0) i |= 31;
+          if (!(left & 1)) continue;
+          const bool draft = i < kTreeMaxDraft;
+          if (draft && !mask_bit(p, t, j_seq, i)) continue;
+          const int pos = draft ? past + i : max(0, past + 1 - p.window) + i - kTreeMaxDraft;
+          if (GEN && p.window >= 1 && (draft && p.positions ? p.positions[sg.seq_t0 + i] : pos) < lo_row) continue;
           const int blk = p.block_table[(size_t)sg.b * p.MB + (pos >> p.log_bs)];
           if (blk < 0 || blk >= p.NB) continue;
           const __half* v =

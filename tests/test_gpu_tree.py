@@ -68,6 +68,8 @@ CASES = {
     "random_mask": dict(past=[333, 1], n=[70, 200], H=4, Hk=2, D=128, bs=32, mask="random", dtype=BF16),
     "mask_wider_than_draft": dict(past=[50], n=[5], H=4, Hk=2, D=64, bs=16, max_draft=100),
     "softcap": dict(past=[300, 20], n=[12, 3], H=4, Hk=2, D=128, bs=16, softcap=5.0, q_std=6.0),
+    "softcap_both_ways": dict(past=[900, 200], n=[12, 60], H=8, Hk=2, D=128, bs=16, softcap=5.5),
+    "softcap_far_above": dict(past=[300, 20], n=[12, 3], H=4, Hk=2, D=64, bs=16, softcap=200.0, dtype=BF16),
     "window": dict(past=[500, 20, 64], n=[12, 30, 64], H=4, Hk=2, D=64, bs=16, window=33),
     "window_of_one": dict(past=[200, 0], n=[9, 4], H=4, Hk=2, D=128, bs=16, window=1),
     "window_wider_than_all": dict(past=[100], n=[9], H=4, Hk=2, D=128, bs=16, window=100000),
@@ -142,6 +144,34 @@ def test_masked_keys_never_reach_a_row(dtype, bad, D, n):
     assert ((got[keep] - ref[keep]).abs() <= tol[keep]).all()
     assert not torch.isfinite(got[touched][..., 5]).any()
     assert u > 0 and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("D,n,window", [(128, [40, 9], 50), (128, [70, 9], 129), (64, [14, 6], 20), (64, [30, 9], 2),
+                                        (256, [40, 9], 75)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_keys_behind_the_window_never_reach_a_row(bad, D, n, window):
+    """Context keys at the edge of the window, which some rows of a tree still admit, and behind it."""
+    c = tree_ref.make_case([190, 140], n, 4, 2, D, 16, window=window, seed=9)
+    # the edge's first two keys, the one before it, and in sequence 1 the last that some row leaves out
+    low = [p - window + 1 for p in c["past"]]
+    victims = [{low[0] - 1, low[0], low[0] + 1}, {low[1] - 1, low[1], int(c["pos"][n[0]:].max()) - window}]
+    victims = [sorted(v & set(range(p))) for v, p in zip(victims, c["past"])]
+    touched = torch.zeros(c["T"], dtype=torch.bool)
+    for fill in (bad, 0.0):
+        for b in range(2):
+            rows = slice(int(c["cum"][b]), int(c["cum"][b + 1]))
+            for p in victims[b]:
+                slot = int(c["table"][b, p // 16]) * 16 + p % 16
+                c["key_cache"].view(-1, 2, D)[slot, :, 3] = fill
+                c["value_cache"].view(-1, 2, D)[slot, :, 5] = fill
+                touched[rows] |= c["pos"][rows] - window < p
+        if fill != 0.0:
+            _, out = attend(c)
+    assert touched.any() and not touched.all()
+    got = out.double().cpu().view(c["T"], 4, D)
+    ref, tol = tree_ref.attention(c)  # (the rows that admit no victim are those of the mended pools)
+    assert ((got[~touched] - ref[~touched]).abs() <= tol[~touched]).all()
+    assert not torch.isfinite(got[touched][..., 5]).any()
 
 
 def test_infinite_value_in_an_admitted_key_keeps_its_channel():
@@ -713,6 +743,10 @@ def test_refusals_of_calls():
                      o.get("T", 3), o.get("out", out)]
     refused("output", op.attention, *a(out=q))
     refused("output", op.attention, *a(out=kc.view(-1, 256)[:3]))
+    refused("positions", op.attention, *a(), positions=out.view(torch.int32).view(-1)[8:])
+    refused("tree_mask", op.attention, *a(), tree_mask=out.view(torch.int32).view(-1)[100:])
+    refused("distance_slopes", op.attention, *a(), distance_slopes=out.view(torch.float32).view(-1)[20:])
+    refused("head_sink", op.attention, *a(), head_sink=out.view(-1)[:4])
     refused("batch", op.attention, *a(batch=0))
     refused("token_count", op.attention, *a(T=4))
     refused("aligned", op.attention, *a(out=torch.empty(3 * 256 + 1, dtype=F16, device="cuda")[1:]))
