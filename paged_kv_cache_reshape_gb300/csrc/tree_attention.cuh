@@ -1225,7 +1225,8 @@ __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_cons
       if (lane < 8) store(row, M, den, acc);
     }
   }
-  if (threadIdx.x == 0) {  // (n_cuts was read above)
+  __syncthreads();  // every warp has read n_cuts
+  if (threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(&p.counters->joined, 1) == (int)gridDim.x - 1) {
       p.counters->n_cuts[0] = 0;
