@@ -516,7 +516,9 @@ typedef struct pa_tree_handle_s* pa_tree_handle;
  * PA_NOT_SUPPORTED: 8-bit caches, the latent layout, packed_qkv, qk_norm,
  * more than 4096 heads.  Allocates the workspace (split-KV partials, error
  * word) on the current device; other calls run there whatever is current.
- * A batch of more than 2^31 key tiles is flagged (PA_DEVERR_KV_BOUND).
+ * Flagged (PA_DEVERR_KV_BOUND): a sequence of 2^26 key tiles (128 keys by up
+ * to 256 query rows of a kv head; 64 by 128 at head_size 256) or more, and a
+ * batch of 2^31.
  * One handle's pa_tree_attention calls share that workspace: calls (and
  * replays of graphs captured from them) on one handle must not overlap on the
  * GPU; use a handle per stream.  pa_tree_write and pa_tree_commit do not use it. */

@@ -438,6 +438,12 @@ def _row_stride(t):
     return stride[0]
 
 
+def _dense(t):
+    if not t.is_contiguous():
+        raise PAError(PA_INVALID_ARGUMENT, "query_out, attention's query and output, and accepted must be contiguous")
+    return t.data_ptr()
+
+
 def pa_rotary(rc, steps, positions, token_count, num_heads, query, query_out, kv_num_heads=0, key=None,
               key_out=None, stream=None):
     """Rotates the rows of query [T, num_heads * D] and key; row strides are the tensors' own."""
@@ -470,7 +476,7 @@ def pa_tree_write(h, rc, steps, positions, query, key, value, query_out, key_cac
                   cumulative_sequence_lengths, past_sequence_lengths, batch, token_count, stream=None):
     st = (_lib or lib()).pa_tree_write(h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query),
                              key.data_ptr(), _row_stride(key), value.data_ptr(), _row_stride(value),
-                             query_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                             _dense(query_out), key_cache.data_ptr(), value_cache.data_ptr(),
                              block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
                              past_sequence_lengths.data_ptr(), batch, token_count, stream)
     if st:
@@ -484,9 +490,9 @@ def pa_tree_attention(h, query, key_cache, value_cache, block_table, cumulative_
                        None if tree_mask is None else tree_mask.data_ptr(),
                        None if distance_slopes is None else distance_slopes.data_ptr(),
                        None if head_sink is None else head_sink.data_ptr())
-    st = (_lib or lib()).pa_tree_attention(h, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+    st = (_lib or lib()).pa_tree_attention(h, _dense(query), key_cache.data_ptr(), value_cache.data_ptr(),
                                  block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
-                                 past_sequence_lengths.data_ptr(), batch, token_count, x, output.data_ptr(), stream)
+                                 past_sequence_lengths.data_ptr(), batch, token_count, x, _dense(output), stream)
     if st:
         _tree_check(st, h)
 
@@ -507,7 +513,7 @@ def pa_tree_commit(h, layers, block_table, past_sequence_lengths, accepted, acce
                    stream=None):
     """accepted [batch, max_accepted] int32 (contiguous), accepted_count [batch]; layers: a layer_pools."""
     st = (_lib or lib()).pa_tree_commit(h, layers.keys, layers.values, layers.num_layers, block_table.data_ptr(),
-                              past_sequence_lengths.data_ptr(), accepted.data_ptr(), accepted_count.data_ptr(),
+                              past_sequence_lengths.data_ptr(), _dense(accepted), accepted_count.data_ptr(),
                               accepted.shape[1], batch, None if new_past is None else new_past.data_ptr(), stream)
     if st:
         _tree_check(st, h)

@@ -50,6 +50,27 @@
 // streams (thread = row = TMEM lane); warps 8 and 11 K and V producers (TMA,
 // one ring of slots in the order of their use), warp 9 TMEM owner and MMA
 // issuer, warp 10 takes chunks, publishes their segments and loads Q.
+//
+// What bounds it (one GB300; 6780 GB/s copied, 1925 TFLOP/s in a plain 16-bit
+// matrix product; calls with their join, inputs not in L2):
+//   64 sequences, 512..4096 keys, 8 tokens, 32/8 heads of 128   95 us  5.7 TB/s  the K/V stream
+//   2 sequences, 100000..131072 keys, 32 tokens, 32/8 heads    143 us  6.2 TB/s  the K/V stream
+//   16 sequences, 1024..8192 keys, 64 tokens, 64/8 heads       141 us  1.09 PFLOP/s
+// The last is bound by each stream's chain S -> softmax -> P -> PV (2.0 us for
+// a key tile of both streams, 1.1 us of it tensor work): the tensor pipe is
+// active 57 % of the time, no other pipe above 30 %.  Handing P over in two
+// halves shortens a tile to 1.74 us in a traced copy but not the call (144 us).
+// What the layout above is worth at the 64 sequences: consecutive chunks by
+// head rather than by range 158 -> 109 us together with one 5-D box per page;
+// K and V from two warps 109 -> 99 us; row replicas (head_size 64, bias) 75 ->
+// 52 us; the equal static ranges against a queue of small chunks, at the 2
+// long sequences, 142 against 154 us.  One sequence of 600 keys and 5 tokens
+// takes 12 us, latency throughout: 3 us to the first S, 3 us for the join.
+//
+// Code size counts: one CTA per SM runs six different roles, and a segment's
+// end is run once per segment by each.  Rarely run loops are therefore not
+// unrolled and waits kept small: with 128 KB of code a segment's end took 4 to
+// 7 us of instruction fetches, with 65 KB 1.5 us.
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -78,8 +99,11 @@ constexpr int kInfoRing = 4;  // segments published ahead of their use
 constexpr int kMaskRing = 16;
 constexpr int kMaxSlots = 12;  // K/V ring slots at most
 constexpr int kJoinChannels = 16;  // channels of the replicas joined at a time
-constexpr int kUnitCost = 2;  // a unit's fixed cost in key tiles
-constexpr int kMinRange = 2;  // a line of less than twice this stays whole
+// A unit's fixed cost in key tiles (64 sequences of 512..4096 keys with 0, 1,
+// 2, 3: 100.1, 99.1, 97.3, 97.0 us when first swept; 95.6 with 2, 96.6 with 3 since).
+constexpr int kUnitCost = 2;
+constexpr int kMaxLen = 1 << 26;  // of a sequence in the line (a window of 32 stays below 2^31)
+constexpr int kMinRange = 2;  // a line of less than twice this stays whole (2 was the best of a sweep)
 
 template <int D>
 struct TreeCfg {
@@ -185,7 +209,9 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, int& bit
     s.lo = p.window >= 1 ? (max(0, s.past + 1 - p.window) & ~(kKeys - 1)) : 0;
     s.nt = (s.past + s.n - s.lo + kKeys - 1) / kKeys;
     s.pairs = (((s.n - 1) * p.inv_unit) >> 20) + 1;  // ceil(n / unit_tokens)
-    s.len = (s.nt + kUnitCost) * s.pairs;
+    const long long len = (long long)(s.nt + kUnitCost) * s.pairs;
+    if (len < kMaxLen) s.len = (int)len;
+    else bits |= PA_DEVERR_KV_BOUND;
   }
   return s;
 }
@@ -205,9 +231,8 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 }
 
 // Bounded mbarrier wait: gives up (returns false) when another role has set
-// *abort, or after kWaitLimit polls, setting it to the wait's site.  (Small:
-// the kernel's code has to stay in the instruction cache, see the end of the
-// file's comment.)
+// *abort, or after kWaitLimit polls, setting it to the wait's site.  (Small,
+// for the code size.)
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
   uint32_t i = 0;
 #pragma unroll 1
@@ -318,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.batch <= kThreads) __syncthreads();  // the groups' starts replace their lengths
       if (lane == 0 && (b0 >> 5) + warp < p.n_groups) groups[(b0 >> 5) + warp] = (int)first;
     }
-    if (before > 0x7fffffffll) {  // 2^31 key tiles: days of work
+    if (before > 0x7fffffffll) {  // 2^31 key tiles: over ten seconds of work
       bits |= PA_DEVERR_KV_BOUND;
       before = 0;
     }
@@ -361,11 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         int bits = 0;
         group = 0;
         load_window(bits);
-        // (32 lengths below 2^26 cannot pass 2^31; a longer one is days of work)
-        if (__reduce_max_sync(0xffffffffu, (unsigned)mine.len) >= 1u << 26) {
-          bits |= PA_DEVERR_KV_BOUND;
-          win_hi = 0;
-        }
         if (bits && blockIdx.x == 0) atomicOr(p.err, bits);
         total = win_hi;
       }
@@ -1148,6 +1168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the pieces (every fourth one), added by shuffles.  Partials are stored
 // channel group by channel group with rows side by side, so both kernels
 // access whole sectors.  The last block to finish clears the counters.
+// Bound by L2: about 8 us for the 47 MB of 144 units of 256 rows of 128
+// channels, of which 3 us are the launch.  (In the main kernel, by whoever
+// writes a unit's last piece: 158 us against 145 at two long sequences.)
 template <int D, bool BF>
 __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_constant__ TreeParams p) {
   const int lane = threadIdx.x & 31, c8 = threadIdx.x >> 5;

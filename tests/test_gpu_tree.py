@@ -219,6 +219,21 @@ def test_bad_device_data_is_flagged_and_skipped():
     assert small.device_error() == pa.PA_DEVERR_Q_BOUND
 
 
+def test_a_sequence_too_long_to_schedule_is_flagged():
+    """2^24 key tiles for each of 256 units (one page that stands for all of a table) are refused on the device."""
+    H, D, bs, n, MB = 128, 256, 256, 256, (1 << 30) // 256
+    cfg = pa.make_config(H, 1, D, bs, 1, MB, 1, n, cache_dtype=pa.PA_CACHE_FP16)
+    op = pa.PagedTree(cfg, n)
+    kc, vc = torch.zeros(1, bs, 1, D, dtype=F16, device="cuda"), torch.zeros(1, bs, 1, D, dtype=F16, device="cuda")
+    out = torch.full((n, H * D), -7.0, dtype=F16, device="cuda")
+    op.attention(torch.zeros_like(out), kc, vc, torch.zeros(1, MB, dtype=torch.int32, device="cuda"),
+                 torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                 torch.tensor([(1 << 30) - n], dtype=torch.int32, device="cuda"), 1, n, out)
+    torch.cuda.synchronize()
+    assert op.device_error() == pa.PA_DEVERR_KV_BOUND
+    assert bool((out == -7.0).all())
+
+
 def test_attention_is_the_same_every_time_and_in_a_graph():
     c = tree_ref.make_case([900, 3000, 17], [20, 8, 40], 8, 2, 128, 16, dtype=BF16, seed=8)
     op = handle(c)
@@ -741,6 +756,9 @@ def test_refusals_of_calls():
     refused("2-D", op.write, *w(q=q.view(3, 4, 64)))
     a = lambda **o: [o.get("q", q), o.get("kc", kc), vc, d["table"], d["cum"], d["past_t"], o.get("batch", 1),  # noqa: E731
                      o.get("T", 3), o.get("out", out)]
+    refused("contiguous", op.write, *w(out=torch.empty(3, 300, dtype=F16, device="cuda")[:, :256]))
+    refused("contiguous", op.attention, *a(out=torch.empty(3, 300, dtype=F16, device="cuda")[:, :256]))
+    refused("contiguous", op.attention, *a(q=torch.empty(3, 300, dtype=F16, device="cuda")[:, :256]))
     refused("output", op.attention, *a(out=q))
     refused("output", op.attention, *a(out=kc.view(-1, 256)[:3]))
     refused("positions", op.attention, *a(), positions=out.view(torch.int32).view(-1)[8:])
