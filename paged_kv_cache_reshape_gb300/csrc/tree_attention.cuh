@@ -55,11 +55,15 @@
 // matrix product; calls with their join, inputs not in L2):
 //   64 sequences, 512..4096 keys, 8 tokens, 32/8 heads of 128   95 us  5.7 TB/s  the K/V stream
 //   2 sequences, 100000..131072 keys, 32 tokens, 32/8 heads    143 us  6.2 TB/s  the K/V stream
-//   16 sequences, 1024..8192 keys, 64 tokens, 64/8 heads       141 us  1.09 PFLOP/s
+//   16 sequences, 1024..8192 keys, 64 tokens, 64/8 heads       138 us  1.12 PFLOP/s
 // The last is bound by each stream's chain S -> softmax -> P -> PV (2.0 us for
 // a key tile of both streams, 1.1 us of it tensor work): the tensor pipe is
-// active 57 % of the time, no other pipe above 30 %.  Handing P over in two
-// halves shortens a tile to 1.74 us in a traced copy but not the call (144 us).
+// active 57 % of the time, no other pipe above 30 %.  What did not help: P
+// handed over in two halves (1.74 us a tile in a traced copy, but the call 144
+// us against 141); at head_size 64 columns of its own for P, so that S runs two
+// tiles ahead (121 against 117 us); the MMA issuer as a whole warp with an
+// elected lane per batch (152 us); the softmax over 32 columns at a time, read
+// twice from tensor memory (half the code; 146 us, with a cap 251 against 227).
 // What the layout above is worth at the 64 sequences: consecutive chunks by
 // head rather than by range 158 -> 109 us together with one 5-D box per page;
 // K and V from two warps 109 -> 99 us; row replicas (head_size 64, bias) 75 ->
@@ -314,7 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  // The allocation is all of tensor memory, so it starts at column 0: as a
+  // constant the columns cost the MMA issuer and the softmax no registers
+  // (16 sequences of 64 drafts 141 -> 138 us, short contexts 75 -> 69).
+  constexpr uint32_t tmem = 0;
+  static_assert(C::kTmemCols == 512, "tensor memory");
 
   griddep_wait();  // lengths, queries and pools may come from the previous kernel
   griddep_launch_dependents();
