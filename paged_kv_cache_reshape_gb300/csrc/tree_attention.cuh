@@ -561,8 +561,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mask = __ballot_sync(0xffffffffu, lane < pages && rc == p.oob_row);
           }
-          if (is_v == v_warp) {  // into the ring's next slot: lane l copies page l
-            if (lane == 0) {
+          if (is_v == v_warp) {  // into the ring's next slot, page by page
+            const int row = is_v && lag && i < cur.nt ? rc_before : rc;
+            uint8_t* const dst = kv_s + at.slot * C::kSlotBytes;
+            const int step = C::kGroupBytes << (log_r - 3);  // of a page
+            // One lane copies all pages, or lane l copies page l (the copies are
+            // issued one after the other either way, from the lanes each with
+            // operands of its own).  With 64 channels the issue of small pages
+            // bounds the K/V stream and one lane is faster (pages of 16: 64
+            // sequences 69.0 -> 63.3 us, two long ones 100 -> 91; of 32, wide
+            // trees: 113.6 -> 116.7); with more channels the lanes are (64
+            // sequences 95.5 against 96.7 us, two long ones 145.4 against 146.2).
+            constexpr bool kOneLane = D == 64;
+            int page_row[kKeys / 16];
+            if constexpr (kOneLane) {
+#pragma unroll
+              for (int g = 0; g < kKeys / 16; ++g) page_row[g] = __shfl_sync(0xffffffffu, row, g);
+            }
+            if (kOneLane ? elect_one() : lane == 0) {
               if (!tree_wait(&ctl->empty[at.slot], at.phase ^ 1, abort, 3)) {
                 ok = false;
               } else {
@@ -571,14 +587,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mbar_arrive(&ctl->mask_full[n_tiles % kMaskRing]);
                 }
                 mbar_arrive_expect_tx(&ctl->full[at.slot], C::kSlotBytes);
+                if constexpr (kOneLane) {
+#pragma unroll
+                  for (int g = 0; g < kKeys / 16; ++g)
+                    if (g < pages) tma_load_5d(dst + g * step, tm, 0, 0, 0, page_row[g] >> 3, cur.k, &ctl->full[at.slot]);
+                }
               }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = kOneLane ? __all_sync(0xffffffffu, ok) : __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            const int row = is_v && lag && i < cur.nt ? rc_before : rc;
-            if (lane < pages)
-              tma_load_5d(kv_s + at.slot * C::kSlotBytes + (lane << (log_r - 3)) * C::kGroupBytes, tm, 0, 0, 0, row >> 3,
-                          cur.k, &ctl->full[at.slot]);
+            if (!kOneLane && lane < pages)
+              tma_load_5d(dst + lane * step, tm, 0, 0, 0, row >> 3, cur.k, &ctl->full[at.slot]);
             issued |= 1u << at.slot;
             phases = (phases & ~(1u << at.slot)) | (at.phase << at.slot);
             ++n_tiles;
