@@ -95,6 +95,9 @@ CASES = {
                                    slopes=True, sink=True, dtype=BF16),
     "d64_everything_64_rows": dict(past=[900, 0, 127], n=[12, 16, 1], H=8, Hk=2, D=64, bs=16, softcap=8.0,
                                    window=200, slopes=True, sink=True, mask="random"),
+    "d64_pages_of_64": dict(past=[700, 63, 64], n=[12, 20, 1], H=4, Hk=2, D=64, bs=64, unmap=[(0, 3)]),
+    "d64_pages_of_256": dict(past=[700, 255, 256], n=[40, 33, 1], H=8, Hk=1, D=64, bs=256, dtype=BF16, sink=True),
+    "d256_pages_of_256": dict(past=[700, 255, 256], n=[12, 20, 1], H=4, Hk=2, D=256, bs=256, dtype=BF16),
     "long_axis_two_tiles": dict(past=[6000], n=[60], H=4, Hk=1, D=128, bs=64),
     "one_head_of_many_pieces": dict(past=[20000], n=[3], H=1, Hk=1, D=128, bs=128),
     "groups_of_128": dict(past=[100], n=[3], H=128, Hk=1, D=64, bs=16),
