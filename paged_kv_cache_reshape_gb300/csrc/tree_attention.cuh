@@ -129,6 +129,9 @@ struct TreeCfg {
   static __host__ __device__ constexpr int s_col(int X) { return X * kKeys; }
   static __host__ __device__ constexpr int o_col(int X) { return 2 * kKeys + (kOneO ? 0 : X * D); }
   static constexpr int kTmemCols = 512;
+  // Whether a V tile's slot may be waited for before the tile's S is, wherever
+  // the tile stands (see mend_v).
+  static __host__ __device__ constexpr bool v_ordered(int rep) { return kOneO ? slots(1, rep) >= 5 : slots(2, rep) >= 7; }
   static __host__ __device__ constexpr int smem_bytes(int q_tiles, int rep) {
     return q_tiles * kQTileBytes + slots(q_tiles, rep) * kSlotBytes + kCtrlBytes + join_bytes(rep);
   }
@@ -747,6 +750,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // S, whose tensor work it then overlaps; by GEN after the softmax, because
       // a window's first V tiles come later than their K (before: 128 sequences
       // of 200..500 keys 62.2 -> 58.9 us; after: a window of 1000 72.2 -> 70.5).
+      //
+      // The wait on the slot's parity means this load only if the slot's load
+      // before it, n_v - S in the segment's order, has landed.  It has if it
+      // belongs to an earlier segment.  Else: products complete in order, so
+      // once S(i) is there so are loads 0 .. 2i - 1, and n_v - S <= 2i - 1 for
+      // every S >= 3.  Before S(i) only the stream's tile before i is known to
+      // be: with two row tiles loads 0 .. 2i - 2 (n_v = 2i + 1; S >= 3), with the
+      // one stream of head_size 256 loads 0 .. 2i - 3 (n_v <= 2i + 2; S >= 5), with
+      // alternating tiles only 0 .. 2i - 5 (n_v <= 2i + 2; S >= 7, where 5 or 6
+      // slots would need S(i) first).
       auto mend_v = [&](int i, int key0) -> bool {
         // no row admits a key below lo_min, and every row the context from lo_edge on
         const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;
@@ -754,6 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's V load, counted from the segment's first, in the ring's order
         const int n_v = two ? 2 * i + 1 : (i == nt - 1 ? 2 * i + 1 : 2 * i + 2);
         const int turn = ring.slot + n_v, sv = turn % S;
+        if constexpr (!GEN && !C::v_ordered(REP))
+          if (!two && n_v >= S && !tree_wait(&ctl->s_full[X], scnt & 1, abort, 16)) return false;
         if (!tree_wait(&ctl->full[sv], ring.phase ^ ((turn / S) & 1), abort, 10)) return false;
         uint8_t* vs = kv_s + sv * C::kSlotBytes;
         const int page_rows = 1 << log_r;
@@ -1294,6 +1309,7 @@ cudaError_t configure() {
   static_assert(C::smem_bytes(1, REP) <= kSmemLimit && C::smem_bytes(kQTiles, REP) <= kSmemLimit, "shared memory");
   static_assert(C::slots(kQTiles, REP) >= 4 && kMaxSlots / 2 + 3 <= kMaskRing, "K/V ring");
   static_assert(2 * C::kKeys + (C::kOneO ? 1 : 2) * D <= C::kTmemCols, "tensor memory");
+  static_assert(C::v_ordered(REP) || (!C::kOneO && C::slots(kQTiles, REP) >= 3), "V slots waited for in order");
   return cudaFuncSetAttribute(tree_kernel<D, BF, GEN, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               std::max(C::smem_bytes(1, REP), C::smem_bytes(kQTiles, REP)));
 }

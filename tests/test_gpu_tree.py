@@ -177,6 +177,64 @@ def test_keys_behind_the_window_never_reach_a_row(bad, D, n, window):
     assert not torch.isfinite(got[touched][..., 5]).any()
 
 
+def ragged(B, lo, hi, n_max, seed, **over):
+    """B sequences of lo..hi keys with trees of 1..n_max drafts, one of n_max among them."""
+    g = torch.Generator().manual_seed(seed)
+    past = torch.randint(lo, hi + 1, (B,), generator=g).tolist()
+    n = torch.randint(1, n_max + 1, (B,), generator=g).tolist()
+    n[B // 2] = n_max
+    return tree_ref.make_case(past, n, over.pop("H"), over.pop("Hk"), over.pop("D"), over.pop("bs"), seed=seed, **over)
+
+
+def attend_repeatedly(c, times=4):
+    """The output of a step whose repetitions are the same bit for bit."""
+    op = handle(c)
+    outs = [attend(c, op)[1]]
+    for _ in range(times - 1):
+        assert torch.equal(attend(c, op)[1].view(torch.int16), outs[0].view(torch.int16))
+    assert op.device_error() == 0
+    return outs[0].double().cpu().view(c["T"], c["H"], c["D"])
+
+
+def assert_close(got, ref, tol):
+    off = (got - ref).abs() - tol
+    assert not got.isnan().any() and off.max() <= 0, f"{int((off > 0).sum())} values off, worst by {off.max():.3g}"
+
+
+# Rows of the widest tree: more than 128 per kv head (the K/V ring has 5 slots beside two tiles of Q), up to 128 (6).
+@pytest.mark.parametrize("n_max,dtype", [(40, BF16), (40, F16), (32, BF16), (24, F16)])
+def test_ragged_trees_over_long_segments(n_max, dtype):
+    """Ranges of about 15 key tiles, so that a segment takes the K/V ring around several times; unused slots of the
+    pages are NaN, and the last tiles' rows behind the sequence must be cleared in the tile itself."""
+    c = ragged(64, 1000, 3000, n_max, 61, H=8, Hk=2, D=128, bs=16, dtype=dtype)
+    ends = [(p + n) % 128 for p, n in zip(c["past"], c["n"])]
+    assert any(0 < e < n for e, n in zip(ends, c["n"]))  # (some drafts lie over two key tiles)
+    ref, tol = tree_ref.attention_by_sequence(c)
+    assert_close(attend_repeatedly(c), ref, tol)
+
+
+@pytest.mark.parametrize("n_max", [40, 32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_masked_keys_never_reach_a_row_over_long_segments(bad, n_max):
+    c = ragged(64, 1000, 3000, n_max, 62, H=8, Hk=2, D=128, bs=16, dtype=BF16)
+    touched = torch.zeros(c["T"], dtype=torch.bool)
+    for fill in (bad, 0.0):
+        for b in range(c["B"]):
+            rows = slice(int(c["cum"][b]), int(c["cum"][b + 1]))
+            for i in {c["n"][b] // 2, c["n"][b] - 1} - {0}:
+                p = c["past"][b] + i
+                slot = int(c["table"][b, p // 16]) * 16 + p % 16
+                c["key_cache"].view(-1, 2, 128)[slot, :, 3] = fill
+                c["value_cache"].view(-1, 2, 128)[slot, :, 5] = fill
+                touched[rows] |= c["rows"][rows, i]
+        if fill != 0.0:
+            got = attend_repeatedly(c)
+    assert touched.any() and not touched.all()
+    ref, tol = tree_ref.attention_by_sequence(c)  # (of the rows that admit none of them)
+    assert_close(got[~touched], ref[~touched], tol[~touched])
+    assert not torch.isfinite(got[touched][..., 5]).any()
+
+
 def test_infinite_value_in_an_admitted_key_keeps_its_channel():
     """An infinite V element of an admitted draft key makes that channel infinite and leaves the others exact."""
     c = tree_ref.make_case([40], [12], 4, 2, 64, 16, seed=6)

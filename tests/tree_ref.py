@@ -125,3 +125,54 @@ def attention(c):
                 if dtype == torch.float16:
                     tol[t, h] += len(kp) * 2.0 ** -25 * v.abs().amax(0)
     return out, tol
+
+
+def attention_by_sequence(c):
+    """attention() with a sequence's rows and keys at once, for long contexts."""
+    H, Hk, D, bs, dtype = c["H"], c["Hk"], c["D"], c["bs"], c["dtype"]
+    u, G = HALF_STEP[dtype], c["H"] // c["Hk"]
+    scale = c["scale"] or 1 / math.sqrt(D)
+    out, tol = torch.zeros(c["T"], H, D).double(), torch.zeros(c["T"], H, D).double()
+    for b in range(c["B"]):
+        past, n, t0 = c["past"][b], c["n"][b], int(c["cum"][b])
+        p = torch.arange(past + n)
+        blocks = c["table"][b].long()[p // bs]
+        p, slots = p[blocks >= 0], (blocks * bs + p % bs)[blocks >= 0]
+        if n == 0 or p.numel() == 0:
+            continue
+        rows = slice(t0, t0 + n)
+        node = p - past
+        draft = node.clamp(min=0)
+        qpos = c["pos"][rows].long() if c["positions"] is not None else past + torch.arange(n)
+        kpos = torch.where(node >= 0, qpos[draft], p)
+        see = torch.where(node >= 0, c["rows"][rows][:, draft], torch.ones(n, 1, dtype=torch.bool))
+        if c["window"] > 0:
+            see = see & (kpos > qpos.clamp(min=past)[:, None] - c["window"])
+        gap = (kpos - qpos[:, None]).double()
+        for k in range(Hk):
+            heads = slice(k * G, (k + 1) * G)
+            q = c["query"].view(c["T"], H, D)[rows, heads].double()
+            K, V = (c[name].view(-1, Hk, D)[slots, k].double() for name in ("key_cache", "value_cache"))
+            x, size = q @ K.T * scale, q.abs() @ K.abs().T * scale  # [n, G, keys]
+            if c["softcap"]:
+                x, size = c["softcap"] * torch.tanh(x / c["softcap"]), size + 2 * c["softcap"]
+            if c["slopes"] is not None:
+                bias = c["slopes"][heads].double()[:, None] * gap[:, None]
+                x, size = x + bias, size + bias.abs()
+            x = torch.where(see[:, None], x, -math.inf)
+            s = c["sink"][heads].double()[:, None] if c["sink"] is not None else torch.full((G, 1), -math.inf).double()
+            top = torch.maximum(x.amax(-1, keepdim=True), s)
+            live = see.any(-1)[:, None, None].expand(n, G, 1)
+            top = torch.where(live, top, 0.0)
+            e = torch.exp(x - top)
+            w8 = e / (e.sum(-1, keepdim=True) + torch.exp(s - top)).clamp(min=1e-300)
+            o, A = w8 @ V, w8 @ V.abs()
+            gone = torch.where(see[:, None], (size + x.abs()) * w8, 0.0).amax(-1, keepdim=True)
+            most = torch.where(w8 > 1e-6, size, 0.0).amax(-1, keepdim=True)
+            w = (D + 8) * 2.0 ** -24 * (gone + most) + 2.0 ** -21
+            t = u * (A + o.abs()) + 2 * w * A
+            if dtype == torch.float16:
+                t = t + see.sum(-1)[:, None, None] * 2.0 ** -25 * V.abs().amax(0)
+            out[rows, heads] = torch.where(live, o, 0.0)
+            tol[rows, heads] = torch.where(live, t, 0.0)
+    return out, tol
