@@ -595,6 +595,23 @@ def test_commit_leaves_bad_paths_and_unmapped_pages():
     assert torch.equal(after, commit_ref(before, {**c, "table": table.clamp(max=c["NB"])}, [[], [], [4], [5]]))
 
 
+@pytest.mark.parametrize("path", [[-9, -5], [-1000000, -999999, -999998], [-5, -9, -3], [15, 0, 1], [1000, 0, 1, 2],
+                                  [0, 5, 1, 2], [-2 ** 31, -2 ** 31 + 1], [2 ** 31 - 1, -1, 0]])
+def test_commit_of_paths_that_ascend_only_in_places(path):
+    """Entries that are above the one before them, but below their own place: nothing is looked up for them, also in
+    the first and the last sequence, whose rows are the table's ends."""
+    c = tree_ref.make_case([0, 20, 251], [20, 20, 5], 2, 2, 64, 16, seed=1)
+    op = handle(c)
+    for victim in range(3):
+        paths = [[1, 3], [0, 2, 4], [1]]
+        paths[victim] = path
+        err, before, after, new = commit(c, paths, op=op)
+        good = [p if b != victim else [] for b, p in enumerate(paths)]
+        assert err == pa.PA_DEVERR_ACCEPTED
+        assert torch.equal(after, commit_ref(before, c, good))
+        assert new.tolist() == [p + len(a) for p, a in zip(c["past"], good)]
+
+
 def test_commit_refusals():
     c = tree_ref.make_case([10], [20], 2, 2, 64, 16)
     op = handle(c)
