@@ -566,8 +566,8 @@ PA_API pa_status pa_tree_attention(pa_tree_handle h, const void* query, const vo
 
 /* For every sequence b and layer l: slot past[b] + i receives the K and V rows
  * of slot past[b] + accepted[b * max_accepted + i], i < accepted_count[b].
- * accepted rows are strictly ascending draft indexes (a path in packed
- * order) with max_accepted <= max_draft_tokens.  key_caches and value_caches
+ * accepted rows are strictly ascending draft indexes below max_draft_tokens
+ * (a path in packed order), with max_accepted <= max_draft_tokens.  key_caches and value_caches
  * are HOST arrays of num_layers device pointers to pools of the handle's
  * geometry, none overlapping another.  new_past [batch] (may be NULL, must
  * not overlap past) receives past[b] + accepted_count[b].  A sequence with a

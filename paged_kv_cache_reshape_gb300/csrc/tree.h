@@ -58,7 +58,7 @@ struct CommitParams {
   const int* past;
   const int* accepted;
   const int* count;
-  int max_accepted, batch, bs, NB, MB;
+  int max_accepted, max_draft, batch, bs, NB, MB;
   int* new_past;
   int* err;
 };

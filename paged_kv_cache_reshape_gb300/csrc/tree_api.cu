@@ -575,6 +575,7 @@ pa_status pa_tree_commit(pa_tree_handle h, void* const* key_caches, void* const*
   p.accepted = accepted;
   p.count = accepted_count;
   p.max_accepted = max_accepted;
+  p.max_draft = h->max_draft;
   p.batch = batch;
   p.bs = c.block_size;
   p.NB = c.num_blocks;

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant_
     // Each entry is looked up only if it can stand at i of an ascending path
     // (a >= i), whatever the others are: slots past + i <= past + a then lie
     // in the sequence's row of the table.
-    if (a <= before || a < i || (long long)past + a >= (long long)p.MB * p.bs) {
+    if (a <= before || a < i || a >= p.max_draft || (long long)past + a >= (long long)p.MB * p.bs) {
       bad = 1;  // (every writer stores the same value)
     } else if (a != i) {
       const int* row = p.block_table + (size_t)b * p.MB;

@@ -612,6 +612,20 @@ def test_commit_of_paths_that_ascend_only_in_places(path):
         assert new.tolist() == [p + len(a) for p, a in zip(c["past"], good)]
 
 
+def test_commit_of_indexes_that_are_no_drafts():
+    """An index at or above max_draft_tokens names no draft, although its slot may be mapped."""
+    c = tree_ref.make_case([10, 20, 40], [20, 11, 9], 2, 2, 64, 16, seed=1)
+    assert c["max_draft"] == 20 and c["MB"] * c["bs"] > 20 + 21
+    op = handle(c)
+    for bad in (20, 21):  # (slots 40 and 41 of the second sequence)
+        paths = [[1, 3], [2, bad], [2]]
+        err, before, after, new = commit(c, paths, op=op)
+        assert err == pa.PA_DEVERR_ACCEPTED
+        assert torch.equal(after, commit_ref(before, c, [[1, 3], [], [2]])) and new.tolist() == [12, 20, 41]
+    err, before, after, new = commit(c, [[1, 19], [2], [2]], op=op)
+    assert err == 0 and torch.equal(after, commit_ref(before, c, [[1, 19], [2], [2]]))
+
+
 def test_commit_refusals():
     c = tree_ref.make_case([10], [20], 2, 2, 64, 16)
     op = handle(c)
