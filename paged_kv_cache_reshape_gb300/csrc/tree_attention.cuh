@@ -1017,7 +1017,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
 
       // ---- end of the segment: the streams show each other their maxima and
-      // sums (needed when they hold the same rows), then O leaves TMEM.
+      // sums (needed when they hold the same rows), then O leaves TMEM.  A row
+      // whose sum is no number (NaN or infinite scores) gets such a maximum,
+      // whatever it met first: -inf means a row without keys, here and in the
+      // joins, and fmaxf passes over a NaN.
+      if (l != l) m_ref = l;
       ctl->ml[X][r] = make_float2(m_ref, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->xchg_full);
@@ -1042,6 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else f0 = f;
           }
         }
+        if (l != l) m_ref = l;
       }
       uint32_t any_bad = lane < 2 * kTreeMaxWords ? ctl->bad[tt & 1][lane] : 0u;
       any_bad = __any_sync(0xffffffffu, any_bad != 0);
@@ -1270,20 +1275,20 @@ __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_cons
         if (ml.x == -INFINITY) continue;
         const float m_new = fmaxf(m, ml.x), f_old = m == -INFINITY ? 0.f : ex2(m - m_new), f = ex2(ml.x - m_new);
         const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        den = f_old == 0.f ? ml.y * f : den * f_old + ml.y * f;
+        den = den * f_old + ml.y * f;  // (a NaN stays one)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = f_old == 0.f ? v[e] * f : acc[e] * f_old + v[e] * f;
+        for (int e = 0; e < 8; ++e) acc[e] = acc[e] * f_old + v[e] * f;
         m = m_new;
       }
       float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
       const float f = m == -INFINITY ? 0.f : ex2(m - M);
-      den = f == 0.f ? 0.f : den * f;
+      den *= f;  // (0 without keys)
       den += __shfl_xor_sync(0xffffffffu, den, 8);
       den += __shfl_xor_sync(0xffffffffu, den, 16);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        acc[e] = f == 0.f ? 0.f : acc[e] * f;
+        acc[e] *= f;
         acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 8);
         acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
       }

@@ -251,6 +251,45 @@ def test_infinite_value_in_an_admitted_key_keeps_its_channel():
     assert ((got - ref).abs() <= tol)[~sees].all()
 
 
+UNFIT = {
+    "one_tile": dict(past=[5], n=[3], H=4, Hk=2), "short": dict(past=[400], n=[5], H=4, Hk=2),
+    "batch": dict(past=[700, 300, 129, 0, 1500], n=[12, 1, 30, 7, 5], H=8, Hk=2),
+    "many_pieces": dict(past=[9000], n=[3], H=2, Hk=1), "two_row_tiles": dict(past=[3000], n=[70], H=8, Hk=2),
+    "two_row_tiles_short": dict(past=[20], n=[70], H=8, Hk=2), "causal": dict(past=[0], n=[9], H=4, Hk=1, mask="none"),
+}
+FORMS = {"plain": {}, "capped": dict(softcap=5.0), "windowed": dict(window=120, sink=True), "biased": dict(slopes=True)}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("name", UNFIT)
+def test_scores_that_are_no_numbers_stay_so(name, D, form):
+    """A NaN in a query row makes the row NaN, one in a key every row that admits it, and an infinite score a row
+    without a cap, however the sequence is cut into pieces; the other rows are as if it were not there."""
+    c = tree_ref.make_case(**UNFIT[name], D=D, bs=16, seed=71, **FORMS[form])
+    ref, tol = tree_ref.attention_by_sequence(c)
+    H, G = c["H"], c["H"] // c["Hk"]
+    q = c["query"].view(c["T"], H, D)
+    lost = torch.zeros(c["T"], H, dtype=torch.bool)
+    for t, h in ((0, 0), (c["T"] - 1, H - 1), (c["T"] // 2, H // 2)):
+        q[t, h, 7] = math.nan
+        lost[t, h] = True
+    if not c["softcap"] and c["past"][0] > 100:  # (enough keys for a score of +inf; tanh takes it back)
+        q[1, 1, 9] = math.inf
+        lost[1, 1] = True
+    b, p = len(c["past"]) - 1, c["past"][-1]  # the last sequence's first draft, seen by its own subtree
+    slot = int(c["table"][b, p // 16]) * 16 + p % 16
+    c["key_cache"].view(-1, c["Hk"], D)[slot, 0, 11] = math.nan
+    rows = slice(int(c["cum"][b]), int(c["cum"][b + 1]))
+    lost[rows, :G] |= c["rows"][rows, 0][:, None]
+    _, out = attend(c)
+    got = out.double().cpu().view(c["T"], H, D)
+    assert lost.any() and (not lost.all() or c["Hk"] == 1)
+    assert got[lost].isnan().all(), f"{int((~got[lost].isnan()).any(-1).sum())} of {int(lost.sum())} rows"
+    if not lost.all():
+        assert_close(got[~lost], ref[~lost], tol[~lost])
+
+
 def test_bad_device_data_is_flagged_and_skipped():
     base = tree_ref.make_case([40, 50, 60], [3, 4, 5], 4, 2, 64, 16, seed=7)
     ref, tol = tree_ref.attention(base)
