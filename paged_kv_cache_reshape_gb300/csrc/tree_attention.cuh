@@ -1026,7 +1026,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->xchg_full);
       if (!tree_wait(&ctl->xchg_full, tt & 1, abort, 11)) break;
-      float f0 = 1.f, f1 = 1.f;  // factors of O_0 and O_1 (one row tile)
+      // Factors of O_0 and O_1 (one row tile), negative where the row met no
+      // key (its O may be 0 * inf); a factor of 0 is applied, so that NaN and
+      // infinities among the values are not lost.
+      float f0 = 1.f, f1 = 1.f;
       if (!two) {
         // over both streams and all replicas of the row
         float2 ml[2 * REP];
@@ -1039,8 +1042,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 2 * REP; ++i) {
-          const float f = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - m_ref);
-          if (f != 0.f) l += f * ml[i].y;
+          const float f = ml[i].x == -INFINITY ? -1.f : ex2(ml[i].x - m_ref);
+          if (!(f < 0.f)) l += f * ml[i].y;
           if ((i >> 1) == (REP > 1 ? r / R : 0)) {
             if (i & 1) f1 = f;
             else f0 = f;
@@ -1098,8 +1101,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              x[e] = f0 == 0.f ? 0.f : x[e] * f0;
-              if (f1 != 0.f) x[e] = fmaf(x[16 + e], f1, x[e]);
+              x[e] = f0 < 0.f ? 0.f : x[e] * f0;
+              if (!(f1 < 0.f)) x[e] = fmaf(x[16 + e], f1, x[e]);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q)  // (the exchange of vectors spreads a warp's stores over the banks)
@@ -1136,8 +1139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!two) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              x[e] = f0 == 0.f ? 0.f : x[e] * f0;
-              if (f1 != 0.f) x[e] = fmaf(x[32 + e], f1, x[e]);
+              x[e] = f0 < 0.f ? 0.f : x[e] * f0;
+              if (!(f1 < 0.f)) x[e] = fmaf(x[32 + e], f1, x[e]);
             }
           }
           if (row_ok) {
@@ -1249,15 +1252,16 @@ __global__ void __launch_bounds__(D / 8 * 32) tree_join_kernel(const __grid_cons
       const float2 ml0 = p.part_ml[at0 * p.part_rows + row], ml1 = p.part_ml[at1 * p.part_rows + row];
       const float4 a0 = o0[0], b0 = o0[p.part_rows], a1 = o1[0], b1 = o1[p.part_rows];
       const float m = fmaxf(ml0.x, ml1.x);
-      const float f0 = ml0.x == -INFINITY ? 0.f : ex2(ml0.x - m), f1 = ml1.x == -INFINITY ? 0.f : ex2(ml1.x - m);
+      // (negative: no key)
+      const float f0 = ml0.x == -INFINITY ? -1.f : ex2(ml0.x - m), f1 = ml1.x == -INFINITY ? -1.f : ex2(ml1.x - m);
       const float v0[8] = {a0.x, a0.y, a0.z, a0.w, b0.x, b0.y, b0.z, b0.w};
       const float v1[8] = {a1.x, a1.y, a1.z, a1.w, b1.x, b1.y, b1.z, b1.w};
-      float acc[8], den = f0 == 0.f ? 0.f : f0 * ml0.y;
-      if (f1 != 0.f) den += f1 * ml1.y;
+      float acc[8], den = f0 < 0.f ? 0.f : f0 * ml0.y;
+      if (!(f1 < 0.f)) den += f1 * ml1.y;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        acc[e] = f0 == 0.f ? 0.f : f0 * v0[e];
-        if (f1 != 0.f) acc[e] += f1 * v1[e];
+        acc[e] = f0 < 0.f ? 0.f : f0 * v0[e];
+        if (!(f1 < 0.f)) acc[e] += f1 * v1[e];
       }
       store(row, m, den, acc);
     } else {

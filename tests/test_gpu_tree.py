@@ -290,6 +290,32 @@ def test_scores_that_are_no_numbers_stay_so(name, D, form):
         assert_close(got[~lost], ref[~lost], tol[~lost])
 
 
+@pytest.mark.parametrize("kind", ["context", "draft"])
+@pytest.mark.parametrize("D,H,Hk,n", [(128, 1, 1, [3, 1]), (128, 8, 2, [60, 40]), (64, 4, 1, [5, 2]), (256, 4, 2, [9, 1]),
+                                      (64, 16, 2, [60, 7]), (128, 16, 16, [3, 1])])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_values_that_are_no_numbers_stay_so_at_any_weight(bad, D, H, Hk, n, kind):
+    """A non-finite V element of a key whose weight is below the smallest float (scores 400 apart, in other pieces of
+    the unit): 0 * inf is NaN in 32 bits, an infinity by the definition, and a number in neither."""
+    c = tree_ref.make_case([5000, 300], n, H, Hk, D, 16, dtype=BF16, mask="none", seed=73)
+    t = 400.0 / (2 * math.sqrt(D) * 3.0)
+    c["query"][:] = 3.0
+    K, V = (c[k].view(-1, Hk, D) for k in ("key_cache", "value_cache"))
+    for b, past in enumerate(c["past"]):
+        for p in range(past + n[b]):
+            slot = int(c["table"][b, p // 16]) * 16 + p % 16
+            K[slot] = -t if (p < past // 2) == (kind == "context") else t  # (half of the keys, whole pieces among them)
+            if p == (17 if kind == "context" else past):
+                V[slot, :, 5] = bad
+    _, out = attend(c)
+    got = out.double().cpu().view(c["T"], H, D)
+    assert not torch.isfinite(got[..., 5]).any()
+    V.nan_to_num_(0.0, 0.0, 0.0)
+    ref, tol = tree_ref.attention_by_sequence(c)
+    others = [ch for ch in range(D) if ch != 5]
+    assert_close(got[..., others], ref[..., others], tol[..., others])
+
+
 def test_bad_device_data_is_flagged_and_skipped():
     base = tree_ref.make_case([40, 50, 60], [3, 4, 5], 4, 2, 64, 16, seed=7)
     ref, tol = tree_ref.attention(base)
