@@ -159,6 +159,9 @@ struct Ctrl {
   // Per segment parity: keys with non-finite V, first the draft tokens, then
   // the context from the window's edge `lo_min` on.
   uint32_t bad[2][2 * kTreeMaxWords];
+  // Per stream, where replicas are joined: whether an output became NaN beside
+  // a sum that is a number, and the channels with a +inf, -inf, NaN value.
+  uint32_t lost[2], found[2][3];
   uint8_t kv_mask[kMaskRing];         // per K/V tile (tile number mod ring): its pages that are unmapped
   uint64_t mask_full[kMaskRing];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
@@ -306,6 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (threadIdx.x < 4 * kTreeMaxWords) ctl->bad[0][threadIdx.x] = 0;
+  if (REP > 1 && threadIdx.x < 2) {
+    ctl->lost[threadIdx.x] = 0;
+    for (int i = 0; i < 3; ++i) ctl->found[threadIdx.x][i] = 0;
+  }
   if (warp == kFetchWarp && lane == 0) prefetch_tmap(&tm_q);
   if (warp == kKWarp && lane == 0) prefetch_tmap(&tm_k);
   if (warp == kVWarp && lane == 0) prefetch_tmap(&tm_v);
@@ -1092,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&ctl->join[X]);
           return tree_wait(&ctl->join[X], joins++ & 1, abort, 14);
         };
-        if (r < R) stat[row] = make_float2(__int_as_float(row_ok ? t * p.H + h : -1), inv);
+        if (r < R) stat[row] = make_float2(__int_as_float(row_ok ? t * p.H + h : -1), l == l ? inv : l);
 #pragma unroll 1
         for (int c = c0; c < c1 && ok; c += kJoinChannels) {
           if (warp_ok) {
@@ -1121,6 +1128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float4 u = red[(k * R + orow) * 4 + (q ^ ((orow >> 1) & 3))];
               v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
             }
+            const float sum = (v.x + v.y) + (v.z + v.w);
+            if (sum != sum && st.y == st.y) ctl->lost[X] = 1;  // (every writer stores the same value)
             if (sg.slot >= 0)
               p.part_o[((size_t)sg.slot * (D / 4) + c / 4 + q) * p.part_rows + orow] = v;
             else
@@ -1130,6 +1139,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && join_all();
         }
         if (!ok) break;
+        if (*static_cast<volatile uint32_t*>(&ctl->lost[X])) {
+          // A replica's P is 0 at the others' keys, and 0 * inf is NaN: an
+          // infinity in a context key was lost.  Which of the stream's channels
+          // hold one (or a NaN, or both signs) is read off the keys that every
+          // row admits and nobody has mended, and put in place of the NaN.
+          static_assert(D / 2 == 32, "a channel per bit");
+          const int first = GEN && p.window >= 1 ? max(sg.key0, min(past - p.window + p.max_draft, past)) : sg.key0;
+          const int last = min(past, sg.key0 + nt * kKeys);
+          uint32_t up = 0, down = 0, none = 0;  // +inf, -inf, NaN
+#pragma unroll 1
+          for (int pos = first + r; pos < last; pos += kRows) {
+            const int blk = p.block_table[(size_t)sg.b * p.MB + (pos >> p.log_bs)];
+            if (blk < 0 || blk >= p.NB) continue;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                p.value_cache + ((((size_t)blk << p.log_bs) + (pos & (p.bs - 1))) * p.Hk + sg.k) * D + c0);
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t two_halves = v[i];
+              if (!nonfinite_halves<BF>(two_halves)) continue;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t half = two_halves >> (16 * e) & 0xffffu;
+                if (!nonfinite16<BF>(half)) continue;
+                const uint32_t bit = 1u << (2 * i + e);
+                if (half & (BF ? 0x7fu : 0x3ffu)) none |= bit;
+                else if (half >> 15) down |= bit;
+                else up |= bit;
+              }
+            }
+          }
+          if (up) atomicOr(&ctl->found[X][0], up);
+          if (down) atomicOr(&ctl->found[X][1], down);
+          if (none) atomicOr(&ctl->found[X][2], none);
+          if (!(ok = join_all())) break;
+          const volatile uint32_t* found = ctl->found[X];
+          up = found[0];
+          down = found[1];
+          none = (up & down) | found[2];
+          if (row_ok && r < R && l == l) {
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+              const uint32_t bit = 1u << (c - c0);
+              if (!((up | down) & ~none & bit)) continue;
+              const float value = up & bit ? INFINITY : -INFINITY;
+              float* po = part ? reinterpret_cast<float*>(part + (size_t)(c / 4) * p.part_rows) + (c & 3) : nullptr;
+              const float was = part ? *po : elem16_to_float(dst[c], BF);
+              if (was == was) continue;
+              if (part) *po = value;
+              else dst[c] = float_to_elem16(value, BF);
+            }
+          }
+          if (!(ok = join_all())) break;
+          if (r < 3) ctl->found[X][r] = 0;
+          if (r == 3) ctl->lost[X] = 0;
+        }
       } else if (warp_ok) {
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {

@@ -316,6 +316,41 @@ def test_values_that_are_no_numbers_stay_so_at_any_weight(bad, D, H, Hk, n, kind
     assert_close(got[..., others], ref[..., others], tol[..., others])
 
 
+@pytest.mark.parametrize("form", ["plain", "windowed"])
+@pytest.mark.parametrize("D,H,Hk,n", [(64, 4, 1, [5, 2, 8, 1]), (64, 8, 2, [12, 16, 3, 1]), (64, 4, 1, [40, 9, 2, 1]),
+                                      (128, 4, 2, [9, 1, 40, 2]), (256, 4, 2, [9, 1, 20, 2])])
+def test_infinite_values_of_context_keys_make_their_channels_infinite(D, H, Hk, n, form):
+    """Infinities of one sign among the values that every row admits give that infinity, of both signs NaN: in one
+    key, in two keys of a tile or of two tiles, and beside an infinite draft."""
+    c = tree_ref.make_case([700, 40, 130, 5000], n, H, Hk, D, 16, dtype=BF16, seed=74, q_std=0.3, sink=True,
+                           window=4000 if form == "windowed" else -1)
+    ref, tol = tree_ref.attention_by_sequence(c)
+    V = c["value_cache"].view(-1, Hk, D)
+
+    def put(b, p, ch, v):
+        V[int(c["table"][b, p // 16]) * 16 + p % 16, :, ch] = v
+
+    want = {5: math.inf, 6: -math.inf, 7: math.inf, D - 1: math.nan, D - 2: math.nan}
+    for b, past in enumerate(c["past"]):
+        put(b, past - 2, 5, math.inf)
+        put(b, past - 1, 6, -math.inf)
+        put(b, past - 30, 6, -math.inf)
+        put(b, past - 3, 7, math.inf)
+        put(b, past - 35, 7, math.inf)
+        put(b, past, 7, math.inf)  # the root of the tree
+        put(b, past - 4, D - 1, math.inf)
+        put(b, past - 39, D - 1, -math.inf)
+        put(b, past - 5, D - 2, math.inf)
+        put(b, past - 1, D - 2, math.nan)
+    _, out = attend(c)
+    got = out.double().cpu().view(c["T"], H, D)
+    for ch, v in want.items():
+        w = torch.full_like(got[..., ch], v)
+        assert torch.equal(got[..., ch].nan_to_num(nan=0.5), w.nan_to_num(nan=0.5)), ch
+    rest = [ch for ch in range(D) if ch not in want]
+    assert_close(got[..., rest], ref[..., rest], tol[..., rest])
+
+
 def test_bad_device_data_is_flagged_and_skipped():
     base = tree_ref.make_case([40, 50, 60], [3, 4, 5], 4, 2, 64, 16, seed=7)
     ref, tol = tree_ref.attention(base)
