@@ -235,6 +235,46 @@ def test_masked_keys_never_reach_a_row_over_long_segments(bad, n_max):
     assert not torch.isfinite(got[touched][..., 5]).any()
 
 
+# Steps whose CTAs work through segments of up to 16 to 68 key tiles, or many short ones, one after the other: the K/V ring and the ring
+# of page masks go around many times, block ids are read 32 at a time, maxima move over a long row, and pieces that
+# are themselves long are joined.
+LONG = {
+    "d128": dict(B=16, lo=5000, hi=6000, n_max=9, H=16, Hk=8, D=128, bs=16, dtype=BF16),
+    "d128_six_slots_from_two_tiles": dict(B=20, lo=1500, hi=6000, n_max=64, H=16, Hk=8, D=128, bs=64),
+    "d128_two_row_tiles": dict(B=12, lo=3000, hi=6000, n_max=100, H=16, Hk=8, D=128, bs=32, dtype=BF16),
+    "d128_growing": dict(B=16, lo=3000, hi=6000, n_max=9, H=16, Hk=8, D=128, bs=16, q_std=6.0),
+    "d128_window": dict(B=16, lo=3000, hi=6000, n_max=40, H=16, Hk=8, D=128, bs=16, window=2500, dtype=BF16),
+    "d128_bias_cap_sink": dict(B=16, lo=3000, hi=6000, n_max=20, H=16, Hk=8, D=128, bs=256, slopes=True, sink=True,
+                               softcap=20.0),
+    "d64_four_replicas": dict(B=16, lo=4000, hi=6000, n_max=12, H=16, Hk=8, D=64, bs=16),
+    "d64_two_replicas": dict(B=16, lo=4000, hi=6000, n_max=30, H=16, Hk=8, D=64, bs=32, dtype=BF16, slopes=True),
+    "d64": dict(B=16, lo=4000, hi=6000, n_max=50, H=16, Hk=8, D=64, bs=128, dtype=BF16),
+    "d64_two_row_tiles": dict(B=12, lo=2000, hi=6000, n_max=90, H=16, Hk=8, D=64, bs=16, softcap=30.0),
+    "d64_window_without_positions": dict(B=16, lo=3000, hi=6000, n_max=30, H=16, Hk=8, D=64, bs=16, window=3001,
+                                         positions=False),
+    "d256": dict(B=8, lo=3000, hi=6000, n_max=20, H=16, Hk=8, D=256, bs=16, dtype=BF16),
+    "d256_rows_over_tiles": dict(B=8, lo=3000, hi=5000, n_max=70, H=16, Hk=8, D=256, bs=64, sink=True),
+    "d256_window": dict(B=8, lo=3000, hi=6000, n_max=20, H=16, Hk=8, D=256, bs=16, window=2000, slopes=True, dtype=BF16),
+    "chunks_above_the_sms": dict(B=4, lo=700, hi=2500, n_max=9, H=100, Hk=100, D=64, bs=16),
+    "segments_of_many_units": dict(B=300, lo=100, hi=900, n_max=20, H=16, Hk=8, D=128, bs=16, dtype=BF16),
+}
+
+
+@pytest.mark.parametrize("unmapped", [False, True])
+@pytest.mark.parametrize("name", LONG)
+def test_long_segments(name, unmapped):
+    over = dict(LONG[name])
+    if unmapped:  # pages of the context, early and late, some of them next to each other
+        over["unmap"] = [(b, p) for b in range(0, over["B"], 2) for p in (0, 1, 3 + b % 4)]
+    c = ragged(seed=80 + len(name), **over)
+    if unmapped:
+        for b in range(1, c["B"], 2):  # the last pages of the context, one before the drafts'
+            last = c["past"][b] // c["bs"] - 1
+            c["table"][b, last], c["table"][b, last // 2] = -1, -1
+    ref, tol = tree_ref.attention_by_sequence(c)
+    assert_close(attend_repeatedly(c, 3), ref, tol)
+
+
 def test_infinite_value_in_an_admitted_key_keeps_its_channel():
     """An infinite V element of an admitted draft key makes that channel infinite and leaves the others exact."""
     c = tree_ref.make_case([40], [12], 4, 2, 64, 16, seed=6)
