@@ -431,10 +431,12 @@ def rotary_steps_tensor(steps, device="cuda"):
     return torch.tensor([v - (1 << 64) if v >> 63 else v for v in steps], dtype=torch.int64, device=device)
 
 
-def _row_stride(t):
+def _row_stride(t, token_count):
     stride = t.stride()
     if len(stride) != 2 or stride[1] != 1:
         raise PAError(PA_INVALID_ARGUMENT, "rows must be 2-D with contiguous columns")
+    if stride[0] == 0 and token_count > 1:  # (an expanded row; in the C call 0 means dense rows)
+        raise PAError(PA_INVALID_ARGUMENT, "rows must not share memory (a row stride of 0)")
     return stride[0]
 
 
@@ -447,12 +449,12 @@ def _dense(t):
 def pa_rotary(rc, steps, positions, token_count, num_heads, query, query_out, kv_num_heads=0, key=None,
               key_out=None, stream=None):
     """Rotates the rows of query [T, num_heads * D] and key; row strides are the tensors' own."""
-    st = (_lib or lib()).pa_rotary(rc, steps.data_ptr(), positions.data_ptr(), token_count, num_heads,
-                         query.data_ptr() if num_heads else None, _row_stride(query) if num_heads else 0,
-                         query_out.data_ptr() if num_heads else None, _row_stride(query_out) if num_heads else 0,
-                         kv_num_heads, key.data_ptr() if kv_num_heads else None,
-                         _row_stride(key) if kv_num_heads else 0, key_out.data_ptr() if kv_num_heads else None,
-                         _row_stride(key_out) if kv_num_heads else 0, stream)
+    st = (_lib or lib()).pa_rotary(
+        rc, steps.data_ptr(), positions.data_ptr(), token_count,
+        num_heads, query.data_ptr() if num_heads else None, _row_stride(query, token_count) if num_heads else 0,
+        query_out.data_ptr() if num_heads else None, _row_stride(query_out, token_count) if num_heads else 0,
+        kv_num_heads, key.data_ptr() if kv_num_heads else None, _row_stride(key, token_count) if kv_num_heads else 0,
+        key_out.data_ptr() if kv_num_heads else None, _row_stride(key_out, token_count) if kv_num_heads else 0, stream)
     if st:
         _check(st)
 
@@ -474,11 +476,11 @@ def pa_tree_destroy(h):
 
 def pa_tree_write(h, rc, steps, positions, query, key, value, query_out, key_cache, value_cache, block_table,
                   cumulative_sequence_lengths, past_sequence_lengths, batch, token_count, stream=None):
-    st = (_lib or lib()).pa_tree_write(h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query),
-                             key.data_ptr(), _row_stride(key), value.data_ptr(), _row_stride(value),
-                             _dense(query_out), key_cache.data_ptr(), value_cache.data_ptr(),
-                             block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
-                             past_sequence_lengths.data_ptr(), batch, token_count, stream)
+    st = (_lib or lib()).pa_tree_write(
+        h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query, token_count),
+        key.data_ptr(), _row_stride(key, token_count), value.data_ptr(), _row_stride(value, token_count),
+        _dense(query_out), key_cache.data_ptr(), value_cache.data_ptr(), block_table.data_ptr(),
+        cumulative_sequence_lengths.data_ptr(), past_sequence_lengths.data_ptr(), batch, token_count, stream)
     if st:
         _tree_check(st, h)
 

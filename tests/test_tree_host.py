@@ -150,3 +150,42 @@ def test_tree_create_without_gpu_and_null_handles():
                            None) == pa.PA_INVALID_ARGUMENT
     assert L.pa_tree_commit(None, None, None, 1, A, A, A, A, 1, 1, None, None) == pa.PA_INVALID_ARGUMENT
     assert "handle" in L.pa_tree_last_error_message(None).decode()
+
+
+def rows(T=3, width=128):
+    import torch
+    return torch.zeros(T, width, dtype=torch.float16)
+
+
+def refused(word, f, *a, **kw):
+    with pytest.raises(pa.PAError) as e:
+        f(*a, **kw)
+    assert e.value.status == pa.PA_INVALID_ARGUMENT and word in e.value.message, e.value
+
+
+@pytest.mark.parametrize("which", ["query", "query_out", "key", "key_out"])
+def test_rotary_refuses_rows_expanded_from_one(which):
+    """A broadcast row has a stride of 0, which in the C call stands for dense rows."""
+    import torch
+    t = dict(query=rows(), query_out=rows(), key=rows(), key_out=rows())
+    t[which] = rows(1).expand(3, 128)
+    refused("stride", pa.pa_rotary, pa.make_rotary_config(64), torch.zeros(32, dtype=torch.int64),
+            torch.zeros(3, dtype=torch.int32), 3, 2, t["query"], t["query_out"], 2, t["key"], t["key_out"])
+
+
+@pytest.mark.parametrize("which", ["query", "key", "value"])
+def test_write_refuses_rows_expanded_from_one(which):
+    import torch
+    t = dict(query=rows(), key=rows(), value=rows())
+    t[which] = rows(1).expand(3, 128)
+    i32 = torch.zeros(4, dtype=torch.int32)
+    refused("stride", pa.pa_tree_write, None, pa.make_rotary_config(64), torch.zeros(32, dtype=torch.int64), i32,
+            t["query"], t["key"], t["value"], rows(), rows(), rows(), i32.view(2, 2), i32, i32, 1, 3)
+
+
+def test_single_rows_have_no_stride():
+    """One row may be a slice of anything, an expanded one too: the calls go on to the next check."""
+    import torch
+    one = rows(1, 256)[:, :128]
+    refused("token_count", pa.pa_rotary, pa.make_rotary_config(64), torch.zeros(32, dtype=torch.int64),
+            torch.zeros(3, dtype=torch.int32), -1, 2, one, one, 2, rows(1).expand(1, 128), one)
