@@ -189,3 +189,58 @@ def test_single_rows_have_no_stride():
     one = rows(1, 256)[:, :128]
     refused("token_count", pa.pa_rotary, pa.make_rotary_config(64), torch.zeros(32, dtype=torch.int64),
             torch.zeros(3, dtype=torch.int32), -1, 2, one, one, 2, rows(1).expand(1, 128), one)
+
+
+def sliced(*size, dtype=None):
+    """A view of that size with gaps between its rows."""
+    import torch
+    big = torch.zeros(size[0], *(2 * s for s in size[1:]), dtype=dtype or torch.int32)
+    return big[tuple(slice(0, s) for s in size)] if len(size) > 1 else torch.zeros(2 * size[0], dtype=big.dtype)[::2]
+
+
+@pytest.mark.parametrize("which", ["steps", "positions", "key_cache", "value_cache", "block_table", "cum", "past"])
+def test_write_refuses_tensors_with_gaps(which):
+    """A slice of a wider block table, or one side of interleaved pools, is not what the C call takes it for."""
+    import torch
+    i32 = torch.zeros(4, dtype=torch.int32)
+    t = dict(steps=torch.zeros(32, dtype=torch.int64), positions=i32, key_cache=torch.zeros(2, 16, 2, 64),
+             value_cache=torch.zeros(2, 16, 2, 64), block_table=i32.view(2, 2), cum=i32, past=i32)
+    t[which] = sliced(*t[which].shape, dtype=t[which].dtype)
+    refused("contiguous", pa.pa_tree_write, None, pa.make_rotary_config(64), t["steps"], t["positions"], rows(), rows(),
+            rows(), rows(), t["key_cache"], t["value_cache"], t["block_table"], t["cum"], t["past"], 1, 3)
+
+
+@pytest.mark.parametrize("which", ["key_cache", "value_cache", "block_table", "cum", "past", "positions", "tree_mask",
+                                   "distance_slopes", "head_sink"])
+def test_attention_refuses_tensors_with_gaps(which):
+    import torch
+    i32 = torch.zeros(4, dtype=torch.int32)
+    t = dict(key_cache=torch.zeros(2, 16, 2, 64), value_cache=torch.zeros(2, 16, 2, 64), block_table=i32.view(2, 2),
+             cum=i32, past=i32, positions=i32, tree_mask=i32.view(2, 2), distance_slopes=torch.zeros(4),
+             head_sink=torch.zeros(4))
+    t[which] = sliced(*t[which].shape, dtype=t[which].dtype)
+    refused("contiguous", pa.pa_tree_attention, None, rows(), t["key_cache"], t["value_cache"], t["block_table"],
+            t["cum"], t["past"], 1, 3, rows(), positions=t["positions"], tree_mask=t["tree_mask"],
+            distance_slopes=t["distance_slopes"], head_sink=t["head_sink"])
+
+
+@pytest.mark.parametrize("which", ["block_table", "past", "accepted", "count", "new_past"])
+def test_commit_refuses_tensors_with_gaps(which):
+    import torch
+    i32 = torch.zeros(4, dtype=torch.int32)
+    t = dict(block_table=i32.view(2, 2), past=i32, accepted=i32.view(2, 2), count=i32, new_past=i32)
+    t[which] = sliced(*t[which].shape)
+    layers = pa.layer_pools([torch.zeros(2, 16, 2, 64)], [torch.zeros(2, 16, 2, 64)])
+    refused("contiguous", pa.pa_tree_commit, None, layers, t["block_table"], t["past"], t["accepted"], t["count"], 1,
+            new_past=t["new_past"])
+
+
+def test_rotary_and_layer_pools_refuse_tensors_with_gaps():
+    import torch
+    pool = torch.zeros(3, 2, 16, 2, 64)
+    refused("contiguous", pa.layer_pools, [pool[:, 0]], [pool[0]])
+    refused("contiguous", pa.layer_pools, [pool[0]], [pool[:, 1]])
+    q, i32 = rows(), torch.zeros(3, dtype=torch.int32)
+    steps = torch.zeros(32, dtype=torch.int64)
+    refused("contiguous", pa.pa_rotary, pa.make_rotary_config(64), sliced(32, dtype=torch.int64), i32, 3, 2, q, q)
+    refused("contiguous", pa.pa_rotary, pa.make_rotary_config(64), steps, sliced(3), 3, 2, q, q)
