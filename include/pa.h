@@ -495,7 +495,8 @@ PA_API void pa_rotary_config_init(pa_rotary_config* rc);
  * heads * D; 0 => heads * D; one row has no stride), so slices of packed rows
  * are taken and written in place.  query_out == query with equal strides
  * rotates in place; an output that overlaps its input in any other way is
- * refused, and so are outputs that overlap each other or the other input.
+ * refused, and so are outputs that overlap each other, the other input,
+ * positions or steps.
  * Overlap is decided by whole ranges of rows, save that two slices of one row
  * layout (equal strides, disjoint columns) do not overlap.  num_heads or
  * kv_num_heads 0 leaves that tensor out (at most 4096 of each).  Runs on the
@@ -528,7 +529,8 @@ PA_API pa_status pa_tree_destroy(pa_tree_handle h);
 /* pa_rotary on Q and K (rc->head_size and dtype must be the handle's), then
  * K and V to slots past[b] + j of the paged pools through block_table (a -1
  * entry writes nothing).  query_out [T, H*D] dense; query_out may be query
- * when query_stride is H*D.  V rows are copied bit for bit.  positions [T]. */
+ * when query_stride is H*D.  V rows are copied bit for bit.  positions [T].
+ * query_out and the pools must not overlap any other input. */
 PA_API pa_status pa_tree_write(pa_tree_handle h, const pa_rotary_config* rc, const uint64_t* steps,
                                const int32_t* positions, const void* query, int64_t query_stride,
                                const void* key, int64_t key_stride, const void* value, int64_t value_stride,
@@ -570,7 +572,7 @@ PA_API pa_status pa_tree_attention(pa_tree_handle h, const void* query, const vo
  * (a path in packed order), with max_accepted <= max_draft_tokens.  key_caches and value_caches
  * are HOST arrays of num_layers device pointers to pools of the handle's
  * geometry, none overlapping another.  new_past [batch] (may be NULL, must
- * not overlap past) receives past[b] + accepted_count[b].  A sequence with a
+ * not overlap any input) receives past[b] + accepted_count[b].  A sequence with a
  * bad path or length is left as it was (new_past = past) and flagged; a -1
  * page moves nothing. */
 PA_API pa_status pa_tree_commit(pa_tree_handle h, void* const* key_caches, void* const* value_caches,

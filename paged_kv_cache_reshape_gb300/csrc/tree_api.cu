@@ -82,6 +82,22 @@ bool overlap(const Rows& a, const Rows& b) {
   return !(x.width <= d && d + y.width <= a.stride);
 }
 
+// What a call writes must be apart from what it reads besides its rows.
+struct Named {
+  Rows rows;
+  const char* name;
+};
+Named plain(const void* p, long long bytes, const char* name) { return {{p, 1, bytes, bytes}, name}; }
+
+template <int W, int R>
+pa_status check_apart(pa_tree_handle h, const Named (&writes)[W], const Named (&reads)[R]) {
+  for (const Named& w : writes)
+    for (const Named& r : reads)
+      if (w.rows.p && r.rows.p && overlap(w.rows, r.rows))
+        return tree_fail(h, PA_INVALID_ARGUMENT, "%s must not overlap %s", w.name, r.name);
+  return PA_OK;
+}
+
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.stride == b.stride && a.width == b.width; }
 
 pa_status check_rotary(pa_tree_handle h, const pa_rotary_config* rc) {
@@ -247,7 +263,7 @@ pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int
   struct { const char* in; const char* out; int heads; const void* src; int64_t ss; void* dst; int64_t ds; } t[2] = {
       {"query", "query_out", num_heads, query, query_stride, query_out, query_out_stride},
       {"key", "key_out", kv_num_heads, key, key_stride, key_out, key_out_stride}};
-  Rows in[2], out[2];
+  Rows in[2] = {}, out[2] = {};
   for (int i = 0; i < 2; ++i) {
     if (t[i].heads == 0) continue;
     if ((st = check_rows(nullptr, t[i].in, t[i].src, token_count, t[i].heads, D, &t[i].ss)) != PA_OK) return st;
@@ -259,6 +275,10 @@ pa_status pa_rotary(const pa_rotary_config* rc, const uint64_t* steps, const int
   }
   if (num_heads && kv_num_heads && (overlap(out[0], out[1]) || overlap(out[0], in[1]) || overlap(out[1], in[0])))
     return pa::host_fail(PA_INVALID_ARGUMENT, "query_out and key_out must not overlap each other or the other input");
+  const Named writes[] = {{out[0], "query_out"}, {out[1], "key_out"}};
+  const Named reads[] = {plain(positions, 4LL * token_count, "positions"),
+                         plain(steps, 8LL * ((rc->rotary_dim ? rc->rotary_dim : D) / 2), "steps")};
+  if ((st = check_apart(nullptr, writes, reads)) != PA_OK) return st;
   pa::RotaryParams p{};
   fill_rotary(&p, rc, steps, positions, token_count);
   p.q = {t[0].src, t[0].dst, t[0].ss, t[0].ds, t[0].heads};
@@ -408,6 +428,13 @@ pa_status pa_tree_write(pa_tree_handle h, const pa_rotary_config* rc, const uint
     if (overlap(*r, kc) || overlap(*r, vc))
       return tree_fail(h, PA_INVALID_ARGUMENT, "the pools must not overlap query, key, value or query_out");
   if (overlap(kc, vc)) return tree_fail(h, PA_INVALID_ARGUMENT, "key_cache and value_cache must not overlap");
+  const Named writes[] = {{qo, "query_out"}, {kc, "key_cache"}, {vc, "value_cache"}};
+  const Named reads[] = {plain(positions, 4LL * token_count, "positions"),
+                         plain(steps, 8LL * ((rc->rotary_dim ? rc->rotary_dim : D) / 2), "steps"),
+                         plain(block_table, 4LL * batch * c.max_blocks_per_seq, "block_table"),
+                         plain(cum, 4LL * (batch + 1), "cumulative_sequence_lengths"),
+                         plain(past, 4LL * batch, "past_sequence_lengths")};
+  if ((st = check_apart(h, writes, reads)) != PA_OK) return st;
   OnDevice g(h->device);
   pa::RotaryParams p{};
   fill_rotary(&p, rc, steps, positions, token_count);
@@ -451,17 +478,15 @@ pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key
   const Rows kc{key_cache, 1, pool, pool}, vc{value_cache, 1, pool, pool};
   if (overlap(o, q) || overlap(o, kc) || overlap(o, vc))
     return tree_fail(h, PA_INVALID_ARGUMENT, "output must not overlap query or the pools");
-  struct { const void* p; long long bytes; const char* name; } reads[] = {
-      {x->positions, 4LL * token_count, "positions"},
-      {x->tree_mask, 4LL * token_count * h->words, "tree_mask"},
-      {x->distance_slopes, 4LL * H, "distance_slopes"},
-      {x->head_sink, 2LL * H, "head_sink"},
-      {block_table, 4LL * batch * c.max_blocks_per_seq, "block_table"},
-      {cum, 4LL * (batch + 1), "cumulative_sequence_lengths"},
-      {past, 4LL * batch, "past_sequence_lengths"}};
-  for (auto& r : reads)
-    if (r.p && overlap(o, Rows{r.p, 1, r.bytes, r.bytes}))
-      return tree_fail(h, PA_INVALID_ARGUMENT, "output must not overlap %s", r.name);
+  const Named writes[] = {{o, "output"}};
+  const Named reads[] = {plain(x->positions, 4LL * token_count, "positions"),
+                         plain(x->tree_mask, 4LL * token_count * h->words, "tree_mask"),
+                         plain(x->distance_slopes, 4LL * H, "distance_slopes"),
+                         plain(x->head_sink, 2LL * H, "head_sink"),
+                         plain(block_table, 4LL * batch * c.max_blocks_per_seq, "block_table"),
+                         plain(cum, 4LL * (batch + 1), "cumulative_sequence_lengths"),
+                         plain(past, 4LL * batch, "past_sequence_lengths")};
+  if ((st = check_apart(h, writes, reads)) != PA_OK) return st;
   OnDevice g(h->device);
   pa::TreeParams p{};
   p.value_cache = static_cast<const __half*>(value_cache);
@@ -545,13 +570,13 @@ pa_status pa_tree_commit(pa_tree_handle h, void* const* key_caches, void* const*
     if (!a.p || !aligned(a.p, 4))
       return tree_fail(h, PA_INVALID_ARGUMENT, "%s must be a 4-byte aligned device pointer", a.name);
   if (!aligned(new_past, 4)) return tree_fail(h, PA_INVALID_ARGUMENT, "new_past must be 4-byte aligned");
-  const Rows np{new_past, 1, 4LL * batch, 4LL * batch};
-  const Rows reads[] = {{past, 1, 4LL * batch, 4LL * batch},
-                        {accepted_count, 1, 4LL * batch, 4LL * batch},
-                        {accepted, 1, 4LL * batch * max_accepted, 4LL * batch * max_accepted}};
-  for (const Rows& r : reads)
-    if (new_past && overlap(np, r))
-      return tree_fail(h, PA_INVALID_ARGUMENT, "new_past must not overlap past_sequence_lengths, accepted or accepted_count");
+  const Named writes[] = {plain(new_past, 4LL * batch, "new_past")};
+  const Named reads[] = {plain(past, 4LL * batch, "past_sequence_lengths"),
+                         plain(accepted_count, 4LL * batch, "accepted_count"),
+                         plain(accepted, 4LL * batch * max_accepted, "accepted"),
+                         plain(block_table, 4LL * batch * c.max_blocks_per_seq, "block_table")};
+  pa_status st = check_apart(h, writes, reads);
+  if (st != PA_OK) return st;
   // Pools: present, aligned and apart from one another.
   const uintptr_t bytes = (uintptr_t)c.num_blocks * c.block_size * c.kv_num_heads * c.head_size * 2;
   std::unique_ptr<uintptr_t[]> store(new (std::nothrow) uintptr_t[2 * (size_t)num_layers]);
@@ -561,6 +586,8 @@ pa_status pa_tree_commit(pa_tree_handle h, void* const* key_caches, void* const*
     for (void* q : {key_caches[l], value_caches[l]}) {
       if (!q || !aligned(q, 16))
         return tree_fail(h, PA_INVALID_ARGUMENT, "layer %d: key_cache and value_cache must be 16-byte aligned device pointers", l);
+      if (new_past && overlap(writes[0].rows, Rows{q, 1, (long long)bytes, (long long)bytes}))
+        return tree_fail(h, PA_INVALID_ARGUMENT, "new_past must not overlap the pools");
       *end++ = reinterpret_cast<uintptr_t>(q);
     }
   }

@@ -791,6 +791,38 @@ def test_commit_refusals():
     assert op.device_error() == 0
 
 
+def test_outputs_over_small_inputs_are_refused():
+    """What a call writes may not be what it reads its lengths, pages or positions from."""
+    c = tree_ref.make_case([33], [3], 4, 2, 64, 16, seed=53)
+    op = handle(c)
+    q, k, v, steps, rc = write_case(c, 64)
+    st = pa.rotary_steps_tensor(steps)
+    kc, vc = c["key_cache"].cuda(), c["value_cache"].cuda()
+    out = torch.zeros_like(q)
+    d = dict(steps=st, positions=c["pos"].cuda(), block_table=c["table"].cuda(), cum=c["cum"].cuda(), past=c["past_t"].cuda())
+    names = dict(cum="cumulative_sequence_lengths", past="past_sequence_lengths")
+    acc, cnt = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def refused(word, f, *a, **kw):
+        with pytest.raises(pa.PAError) as e:
+            f(*a, **kw)
+        assert e.value.status == pa.PA_INVALID_ARGUMENT and word in e.value.message, e.value
+
+    for name in d:
+        for where, big in (("query_out", out), ("key_cache", kc), ("value_cache", vc)):
+            t = dict(d)
+            t[name] = big.view(-1).view(d[name].dtype)[8:8 + d[name].numel()].view(d[name].shape)
+            refused(f"{where} must not overlap {names.get(name, name)}", op.write, rc, t["steps"], t["positions"], q, k, v, out,
+                    kc, vc, t["block_table"], t["cum"], t["past"], 1, 3)
+    layers = pa.layer_pools([kc], [vc])
+    refused("new_past must not overlap block_table", op.commit, layers, d["block_table"], d["past"], acc, cnt, 1,
+            new_past=d["block_table"].view(-1)[1:2])
+    for pool in (kc, vc):
+        refused("new_past must not overlap the pools", op.commit, layers, d["block_table"], d["past"], acc, cnt, 1,
+                new_past=pool.view(-1).view(torch.int32)[40:41])
+    assert op.device_error() == 0
+
+
 # ---------------------------------------------------------------- one step after the other
 
 

@@ -244,3 +244,14 @@ def test_rotary_and_layer_pools_refuse_tensors_with_gaps():
     steps = torch.zeros(32, dtype=torch.int64)
     refused("contiguous", pa.pa_rotary, pa.make_rotary_config(64), sliced(32, dtype=torch.int64), i32, 3, 2, q, q)
     refused("contiguous", pa.pa_rotary, pa.make_rotary_config(64), steps, sliced(3), 3, 2, q, q)
+
+
+@pytest.mark.parametrize("over,word", [
+    (dict(positions=A + (1 << 17)), "query_out must not overlap positions"),
+    (dict(positions=A + (1 << 19) + 380), "key_out must not overlap positions"),
+    (dict(steps=A + (1 << 17) + 760), "query_out must not overlap steps"),
+    (dict(steps=A + (1 << 19) - 248), "key_out must not overlap steps"),
+])
+def test_rotary_refuses_outputs_over_its_tables(over, word):
+    st, msg = rotary(**over)
+    assert st == pa.PA_INVALID_ARGUMENT and word in msg, (st, msg)
