@@ -260,6 +260,18 @@ LONG = {
 }
 
 
+@pytest.mark.parametrize("D,H,Hk", [(64, 2, 1), (128, 1, 1), (256, 2, 1)])
+def test_more_sequences_than_32_groups(D, H, Hk):
+    """2500 sequences, most of them empty: the schedule looks through groups of 32 sequences, 32 at a time."""
+    g = torch.Generator().manual_seed(81)
+    n = (torch.randint(0, 4, (2500,), generator=g) * (torch.rand(2500, generator=g) < 0.2)).tolist()
+    n[1000:1200] = [0] * 200
+    n[-40:] = [0] * 40
+    c = tree_ref.make_case(torch.randint(0, 60, (2500,), generator=g).tolist(), n, H, Hk, D, 16, dtype=BF16, seed=81)
+    ref, tol = tree_ref.attention_by_sequence(c)
+    assert_close(attend_repeatedly(c, 2), ref, tol)
+
+
 @pytest.mark.parametrize("unmapped", [False, True])
 @pytest.mark.parametrize("name", LONG)
 def test_long_segments(name, unmapped):
