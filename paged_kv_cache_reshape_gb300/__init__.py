@@ -440,22 +440,26 @@ def _row_stride(t, token_count):
     return stride[0]
 
 
-def _dense(t):
+def _gaps():
+    raise PAError(PA_INVALID_ARGUMENT, "tensors must be contiguous (save rows of Q, K and V in pa_rotary and "
+                                       "pa_tree_write)")
+
+
+def _optional(t):
+    if t is None:
+        return None
     if not t.is_contiguous():
-        raise PAError(PA_INVALID_ARGUMENT, "tensors must be contiguous (save rows of Q, K and V in pa_rotary and "
-                                           "pa_tree_write)")
+        _gaps()
     return t.data_ptr()
-
-
-def _dense_or_none(t):
-    return None if t is None else _dense(t)
 
 
 def pa_rotary(rc, steps, positions, token_count, num_heads, query, query_out, kv_num_heads=0, key=None,
               key_out=None, stream=None):
     """Rotates the rows of query [T, num_heads * D] and key; row strides are the tensors' own."""
+    if not (steps.is_contiguous() and positions.is_contiguous()):
+        _gaps()
     st = (_lib or lib()).pa_rotary(
-        rc, _dense(steps), _dense(positions), token_count,
+        rc, steps.data_ptr(), positions.data_ptr(), token_count,
         num_heads, query.data_ptr() if num_heads else None, _row_stride(query, token_count) if num_heads else 0,
         query_out.data_ptr() if num_heads else None, _row_stride(query_out, token_count) if num_heads else 0,
         kv_num_heads, key.data_ptr() if kv_num_heads else None, _row_stride(key, token_count) if kv_num_heads else 0,
@@ -481,11 +485,16 @@ def pa_tree_destroy(h):
 
 def pa_tree_write(h, rc, steps, positions, query, key, value, query_out, key_cache, value_cache, block_table,
                   cumulative_sequence_lengths, past_sequence_lengths, batch, token_count, stream=None):
+    # (checked in one expression: the host's time bounds the smallest steps)
+    if not (steps.is_contiguous() and positions.is_contiguous() and query_out.is_contiguous()
+            and key_cache.is_contiguous() and value_cache.is_contiguous() and block_table.is_contiguous()
+            and cumulative_sequence_lengths.is_contiguous() and past_sequence_lengths.is_contiguous()):
+        _gaps()
     st = (_lib or lib()).pa_tree_write(
-        h, rc, _dense(steps), _dense(positions), query.data_ptr(), _row_stride(query, token_count),
+        h, rc, steps.data_ptr(), positions.data_ptr(), query.data_ptr(), _row_stride(query, token_count),
         key.data_ptr(), _row_stride(key, token_count), value.data_ptr(), _row_stride(value, token_count),
-        _dense(query_out), _dense(key_cache), _dense(value_cache), _dense(block_table),
-        _dense(cumulative_sequence_lengths), _dense(past_sequence_lengths), batch, token_count, stream)
+        query_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_table.data_ptr(),
+        cumulative_sequence_lengths.data_ptr(), past_sequence_lengths.data_ptr(), batch, token_count, stream)
     if st:
         _tree_check(st, h)
 
@@ -493,13 +502,15 @@ def pa_tree_write(h, rc, steps, positions, query, key, value, query_out, key_cac
 def pa_tree_attention(h, query, key_cache, value_cache, block_table, cumulative_sequence_lengths,
                       past_sequence_lengths, batch, token_count, output, positions=None, tree_mask=None,
                       distance_slopes=None, head_sink=None, stream=None):
-    x = pa_tree_inputs(_dense_or_none(positions),
-                       _dense_or_none(tree_mask),
-                       _dense_or_none(distance_slopes),
-                       _dense_or_none(head_sink))
-    st = (_lib or lib()).pa_tree_attention(h, _dense(query), _dense(key_cache), _dense(value_cache),
-                                 _dense(block_table), _dense(cumulative_sequence_lengths),
-                                 _dense(past_sequence_lengths), batch, token_count, x, _dense(output), stream)
+    if not (query.is_contiguous() and output.is_contiguous() and key_cache.is_contiguous()
+            and value_cache.is_contiguous() and block_table.is_contiguous()
+            and cumulative_sequence_lengths.is_contiguous() and past_sequence_lengths.is_contiguous()):
+        _gaps()
+    x = pa_tree_inputs(_optional(positions), _optional(tree_mask), _optional(distance_slopes), _optional(head_sink))
+    st = (_lib or lib()).pa_tree_attention(
+        h, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_table.data_ptr(),
+        cumulative_sequence_lengths.data_ptr(), past_sequence_lengths.data_ptr(), batch, token_count, x,
+        output.data_ptr(), stream)
     if st:
         _tree_check(st, h)
 
@@ -512,16 +523,21 @@ class layer_pools:
         if len(self.tensors[0]) != len(self.tensors[1]):
             raise PAError(PA_INVALID_ARGUMENT, "key_caches and value_caches must have one pool per layer each")
         self.num_layers = len(self.tensors[0])
-        self.keys, self.values = ((ctypes.c_void_p * self.num_layers)(*[_dense(t) for t in ts])
+        if not all(t.is_contiguous() for ts in self.tensors for t in ts):
+            _gaps()
+        self.keys, self.values = ((ctypes.c_void_p * self.num_layers)(*[t.data_ptr() for t in ts])
                                   for ts in self.tensors)
 
 
 def pa_tree_commit(h, layers, block_table, past_sequence_lengths, accepted, accepted_count, batch, new_past=None,
                    stream=None):
     """accepted [batch, max_accepted] int32 (contiguous), accepted_count [batch]; layers: a layer_pools."""
-    st = (_lib or lib()).pa_tree_commit(h, layers.keys, layers.values, layers.num_layers, _dense(block_table),
-                              _dense(past_sequence_lengths), _dense(accepted), _dense(accepted_count),
-                              accepted.shape[1], batch, _dense_or_none(new_past), stream)
+    if not (block_table.is_contiguous() and past_sequence_lengths.is_contiguous() and accepted.is_contiguous()
+            and accepted_count.is_contiguous()):
+        _gaps()
+    st = (_lib or lib()).pa_tree_commit(
+        h, layers.keys, layers.values, layers.num_layers, block_table.data_ptr(), past_sequence_lengths.data_ptr(),
+        accepted.data_ptr(), accepted_count.data_ptr(), accepted.shape[1], batch, _optional(new_past), stream)
     if st:
         _tree_check(st, h)
 
