@@ -54,8 +54,9 @@
 // What bounds it (one GB300; 6780 GB/s copied, 1925 TFLOP/s in a plain 16-bit
 // matrix product; calls with their join, inputs not in L2):
 //   64 sequences, 512..4096 keys, 8 tokens, 32/8 heads of 128   95 us  5.7 TB/s  the K/V stream
-//   2 sequences, 100000..131072 keys, 32 tokens, 32/8 heads    143 us  6.2 TB/s  the K/V stream
-//   16 sequences, 1024..8192 keys, 64 tokens, 64/8 heads       138 us  1.12 PFLOP/s
+//   2 sequences, 100000..131072 keys, 32 tokens, 32/8 heads    145 us  6.2 TB/s  the K/V stream
+//   16 sequences, 1024..8192 keys, 64 tokens, 64/8 heads       138 us  1.12 PFLOP/s in a few dozen calls;
+//                            146 to 151 us, 1.02 to 1.06 PFLOP/s, in a thousand: the power cap lowers the clock
 // The last is bound by each stream's chain S -> softmax -> P -> PV (2.0 us for
 // a key tile of both streams, 1.1 us of it tensor work): the tensor pipe is
 // active 57 % of the time, no other pipe above 30 %.  What did not help: P
@@ -129,8 +130,7 @@ struct TreeCfg {
   static __host__ __device__ constexpr int s_col(int X) { return X * kKeys; }
   static __host__ __device__ constexpr int o_col(int X) { return 2 * kKeys + (kOneO ? 0 : X * D); }
   static constexpr int kTmemCols = 512;
-  // Whether a V tile's slot may be waited for before the tile's S is, wherever
-  // the tile stands (see mend_v).
+  // Whether V's slot may be waited for before S is also where tiles alternate (see mend_v).
   static __host__ __device__ constexpr bool v_ordered(int rep) { return kOneO ? slots(1, rep) >= 5 : slots(2, rep) >= 7; }
   static __host__ __device__ constexpr int smem_bytes(int q_tiles, int rep) {
     return q_tiles * kQTileBytes + slots(q_tiles, rep) * kSlotBytes + kCtrlBytes + join_bytes(rep);
@@ -753,20 +753,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Zero V rows that no row admits by position, take non-finite values out of
       // rows that only some admit: the drafts, and the context at the window's
       // edge (once per tile: stream 0 when both use it).  Unmapped pages and
-      // pages behind the sequence are zero already.  Called before the wait for
-      // S, whose tensor work it then overlaps; by GEN after the softmax, because
-      // a window's first V tiles come later than their K (before: 128 sequences
-      // of 200..500 keys 62.2 -> 58.9 us; after: a window of 1000 72.2 -> 70.5).
+      // pages behind the sequence are zero already.
       //
-      // The wait on the slot's parity means this load only if the slot's load
-      // before it, n_v - S in the segment's order, has landed.  It has if it
-      // belongs to an earlier segment.  Else: products complete in order, so
-      // once S(i) is there so are loads 0 .. 2i - 1, and n_v - S <= 2i - 1 for
-      // every S >= 3.  Before S(i) only the stream's tile before i is known to
-      // be: with two row tiles loads 0 .. 2i - 2 (n_v = 2i + 1; S >= 3), with the
-      // one stream of head_size 256 loads 0 .. 2i - 3 (n_v <= 2i + 2; S >= 5), with
-      // alternating tiles only 0 .. 2i - 5 (n_v <= 2i + 2; S >= 7, where 5 or 6
-      // slots would need S(i) first).
+      // When: with GEN after the softmax, because a window's first V tiles come
+      // later than their K (before it: a window of 1000 70.5 -> 72.2 us).  Else
+      // before the wait for S, whose tensor work it then overlaps (head_size 64,
+      // 128 sequences of 200..500 keys 46.2 -> 44.6 us, of 20..100 34.6 -> 33.6),
+      // where that is sound.  The wait on the slot's parity means this load only
+      // if the slot's load before it, n_v - S in the segment's order, has
+      // landed.  It has if it belongs to an earlier segment.  Else: products
+      // complete in order, so once S(i) is there so are loads 0 .. 2i - 1, and
+      // n_v - S <= 2i - 1 for every S >= 3.  Before S(i) only the stream's tile
+      // before i is known to be: with two row tiles loads 0 .. 2i - 2 (n_v =
+      // 2i + 1; S >= 3), with the one stream of head_size 256 loads 0 .. 2i - 3
+      // (n_v <= 2i + 2; S >= 5), with alternating tiles only 0 .. 2i - 5 (n_v <=
+      // 2i + 2; S >= 7).  Alternating tiles of head_size 128 have 5 or 6 slots and
+      // wait for S(i) (36.9 -> 37.1 us for units of one tile, nothing elsewhere).
       auto mend_v = [&](int i, int key0) -> bool {
         // no row admits a key below lo_min, and every row the context from lo_edge on
         const int lo_min = GEN && p.window >= 1 ? max(0, past + 1 - p.window) : 0;
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_v = two ? 2 * i + 1 : (i == nt - 1 ? 2 * i + 1 : 2 * i + 2);
         const int turn = ring.slot + n_v, sv = turn % S;
         if constexpr (!GEN && !C::v_ordered(REP))
-          if (!two && n_v >= S && !tree_wait(&ctl->s_full[X], scnt & 1, abort, 16)) return false;
+          if (!two && !tree_wait(&ctl->s_full[X], scnt & 1, abort, 16)) return false;
         if (!tree_wait(&ctl->full[sv], ring.phase ^ ((turn / S) & 1), abort, 10)) return false;
         uint8_t* vs = kv_s + sv * C::kSlotBytes;
         const int page_rows = 1 << log_r;
