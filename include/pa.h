@@ -557,9 +557,12 @@ typedef struct {
  * output = sum softmax(x) v, 0 when nothing is admitted.  A key that a row
  * does not admit never reaches that row, whatever its K and V hold (under a
  * window this holds for rows at positions below past[b] + max_draft_tokens;
- * a row further on needs finite V at its window's edge).  query, output
- * [T, H*D]; output must not overlap the inputs.  P is rounded to the 16-bit type for the P*V
- * contraction; scores, sums and the output accumulate in fp32. */
+ * a row further on needs finite V at its window's edge).  A score that is
+ * NaN or +inf makes its row NaN, and a non-finite V of an admitted key that
+ * channel of the row.  query, output [T, H*D]; output must not overlap the
+ * inputs.  P is rounded to the 16-bit type for the P*V contraction; scores,
+ * sums and the output accumulate in fp32 (a distance bias is held to 2^-22 of
+ * |slope| (128 + |kpos - qpos|)). */
 PA_API pa_status pa_tree_attention(pa_tree_handle h, const void* query, const void* key_cache,
                                    const void* value_cache, const int32_t* block_table,
                                    const int32_t* cumulative_sequence_lengths,
@@ -569,9 +572,9 @@ PA_API pa_status pa_tree_attention(pa_tree_handle h, const void* query, const vo
 /* For every sequence b and layer l: slot past[b] + i receives the K and V rows
  * of slot past[b] + accepted[b * max_accepted + i], i < accepted_count[b].
  * accepted rows are strictly ascending draft indexes below max_draft_tokens
- * (a path in packed order), with max_accepted <= max_draft_tokens.  key_caches and value_caches
- * are HOST arrays of num_layers device pointers to pools of the handle's
- * geometry, none overlapping another.  new_past [batch] (may be NULL, must
+ * (a path in packed order), with max_accepted <= max_draft_tokens.
+ * key_caches and value_caches are HOST arrays of num_layers device pointers
+ * to pools of the handle's geometry, none overlapping another.  new_past [batch] (may be NULL, must
  * not overlap any input) receives past[b] + accepted_count[b].  A sequence with a
  * bad path or length is left as it was (new_past = past) and flagged; a -1
  * page moves nothing. */
