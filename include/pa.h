@@ -726,11 +726,14 @@ PA_API pa_status pa_pages_fork(pa_pages_handle h, void* const* pools, int num_po
 
 /* Row r, of lengths[r] positions, becomes one of lengths[r] + delta[r], in
  * place: missing pages of the new positions are taken from the free ones,
- * entries behind the last position give theirs back (delta = -length frees
- * the row), and a page that the next position falls into while other rows
- * refer to it is replaced by a copy.  Entries without a page below lengths[r]
- * stay as they are.  A row whose pages are not all to be had is left as it
- * was and flagged (PA_DEVERR_PAGES), and so are later rows that need any.
+ * and entries behind the last position give theirs back (delta = -length frees
+ * the row).  A page of new positions that other entries refer to before the
+ * call (a reference count above 1) is replaced by a fresh one, which receives
+ * its bytes where positions below lengths[r] lie in it too.  An entry without
+ * a page that holds a position below lengths[r] stays as it is.  A row whose
+ * pages are not all to be had is left as it was and flagged (PA_DEVERR_PAGES),
+ * and so are later rows that need any; so is a row with a bad length, old or
+ * new (PA_DEVERR_PAST, PA_DEVERR_KV_BOUND).
  * new_lengths (lengths itself is allowed) receives the lengths that hold. */
 PA_API pa_status pa_pages_resize(pa_pages_handle h, void* const* pools, int num_pools, int32_t* block_table,
                                  const int32_t* lengths, const int32_t* delta, int rows, int32_t* new_lengths,

@@ -175,8 +175,16 @@ __device__ __forceinline__ bool resized(const PagesParams& p, int r, int* was, i
   return a >= 0 && a <= most && b >= 0 && b <= most;
 }
 
-// The shared page that a row would write next, or -1: what holds positions
-// from `was` on while other rows still refer to it.
+// Whether a growing row's entry c, which new positions fall into, has to
+// become a fresh page: it has none, or one that other rows refer to as well.
+// (An entry that holds positions below `was` too and has no page stays so.)
+__device__ __forceinline__ bool wants_page(const PagesParams& p, const int* ref, const int* entry, int c, int was) {
+  const int page = page_at(entry, p.NB, p.err);
+  return page >= 0 ? ref[page] > 1 : (long long)c * p.bs >= was;
+}
+
+// The shared page whose bytes a growing row takes along into a fresh one, or
+// -1: it holds positions on both sides of `was`.
 __device__ __forceinline__ int shared_page(const PagesParams& p, int r, int was, int now) {
   if (now <= was || was % p.bs == 0) return -1;
   const int page = page_at(p.table + (size_t)r * p.MB + was / p.bs, p.NB, p.err);
@@ -195,9 +203,9 @@ __device__ void plan_resize(const PagesParams& p, int* shared) {
     if (!resized(p, r, &was, &now)) {
       atomicOr(p.err, was < 0 ? PA_DEVERR_PAST : PA_DEVERR_KV_BOUND);
     } else if (pages_of(now, p.bs) - pages_of(was, p.bs) <= kFew) {
-      need = shared_page(p, r, was, now) >= 0;
-      for (int c = pages_of(was, p.bs); c < pages_of(now, p.bs); ++c)
-        need += page_at(p.table + (size_t)r * p.MB + c, p.NB, p.err) < 0;
+      need = 0;
+      for (int c = was / p.bs; now > was && c < pages_of(now, p.bs); ++c)
+        need += wants_page(p, p.ref, p.table + (size_t)r * p.MB + c, c, was);
       need = min(need, p.NB + 1);  // (more than there are is too many)
     }
     p.w.entries[r] = need;
@@ -206,9 +214,9 @@ __device__ void plan_resize(const PagesParams& p, int* shared) {
   for (int r = warp; r < p.rows; r += kPlan / 32) {
     int was, now, need = 0;
     if (!resized(p, r, &was, &now) || pages_of(now, p.bs) - pages_of(was, p.bs) <= kFew) continue;
-    for (int c = pages_of(was, p.bs) + lane; c < pages_of(now, p.bs); c += 32)
-      need += page_at(p.table + (size_t)r * p.MB + c, p.NB, p.err) < 0;
-    need = __reduce_add_sync(0xffffffffu, need) + (shared_page(p, r, was, now) >= 0);
+    for (int c = was / p.bs + lane; c < pages_of(now, p.bs); c += 32)
+      need += wants_page(p, p.ref, p.table + (size_t)r * p.MB + c, c, was);
+    need = __reduce_add_sync(0xffffffffu, need);
     if (lane == 0) p.w.entries[r] = min(need, p.NB + 1);
   }
   __syncthreads();
@@ -221,8 +229,8 @@ __device__ void plan_resize(const PagesParams& p, int* shared) {
     want = (int)min((long long)want + total, (long long)INT_MAX / 2);
   }
   const int got = find_free(p.ref, p.NB, min(want, p.NB), p.w.free_list, shared, head);
-  // Rows whose pages are all there are served; a shared page is copied to
-  // the row's first fresh one.
+  // Rows whose pages are all there are served, entries in their order; the
+  // page that is copied is the first of them.
   int moved = 0;
   for (int base = 0; base < p.rows; base += kPlan) {
     const int r = base + threadIdx.x;
@@ -287,8 +295,9 @@ __global__ void __launch_bounds__(kPlan) plan_kernel(const __grid_constant__ Pag
   __shared__ int shared[kPlan / 32 + 1];
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x > 0) {  // the other blocks carry the counts over
-    for (int i = (blockIdx.x - 1) * kPlan + threadIdx.x; i < p.NB; i += (gridDim.x - 1) * kPlan) p.ref_out[i] = p.ref[i];
+  if (blockIdx.x > 0) {  // the other blocks carry the counts over, or keep them as they were
+    int* to = OP == kPageResize ? p.w.place : p.ref_out;
+    for (int i = (blockIdx.x - 1) * kPlan + threadIdx.x; i < p.NB; i += (gridDim.x - 1) * kPlan) to[i] = p.ref[i];
     return;
   }
   if constexpr (OP == kPageCopy) plan_copy(p, shared);
@@ -328,30 +337,20 @@ __device__ void apply_resize(const PagesParams& p, long long warp, long long war
     const int now = p.lengths_out[r];
     const int was = (int)((long long)now - p.delta[r]);
     int at = p.w.fresh[r];
-    int pages = pages_of(was, p.bs);
-    // The shared page was planned for the first fresh one.
-    const int need = p.w.entries[r];
-    int missing = 0;
-    for (int c = pages + lane; c < pages_of(now, p.bs); c += 32) missing += row[c] < 0 || row[c] >= p.NB;
-    missing = __reduce_add_sync(0xffffffffu, missing);
-    if (need > missing) {
-      if (lane == 0) {
-        atomicAdd(&p.ref_out[row[was / p.bs]], -1);
-        row[was / p.bs] = p.w.free_list[at];
-        p.ref_out[p.w.free_list[at]] = 1;
-      }
-      ++at;
-    }
-    for (int c0 = pages; c0 < pages_of(now, p.bs); c0 += 32) {
+    // As planned: the counts are those of before the call (place), which this
+    // launch changes.
+    const int end = p.w.entries[r] > 0 ? pages_of(now, p.bs) : 0;
+    for (int c0 = was / p.bs; c0 < end; c0 += 32) {
       const int c = c0 + lane;
-      const bool gap = c < pages_of(now, p.bs) && (row[c] < 0 || row[c] >= p.NB);
-      const unsigned gaps = __ballot_sync(0xffffffffu, gap);
-      if (gap) {
-        const int page = p.w.free_list[at + __popc(gaps & ((1u << lane) - 1))];
+      const bool takes = c < end && wants_page(p, p.w.place, row + c, c, was);
+      const unsigned takers = __ballot_sync(0xffffffffu, takes);
+      if (takes) {
+        const int old = row[c], page = p.w.free_list[at + __popc(takers & ((1u << lane) - 1))];
+        if (old >= 0 && old < p.NB) atomicAdd(&p.ref_out[old], -1);
         row[c] = page;
         p.ref_out[page] = 1;
       }
-      at += __popc(gaps);
+      at += __popc(takers);
     }
     for (int c = pages_of(now, p.bs) + lane; c < p.MB; c += 32) {
       const int page = page_at(row + c, p.NB, p.err);
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(kApply) apply_kernel(const __grid_constant__ P
 }  // namespace
 
 cudaError_t launch_page_plan(PageOp op, const PagesParams& p, cudaStream_t s) {
-  const bool carry = op != kPageCopy && p.ref_out != p.ref;
+  const bool carry = op == kPageResize || (op != kPageCopy && p.ref_out != p.ref);
   const dim3 grid(1 + (carry ? std::min(64, (p.NB + kPlan - 1) / kPlan) : 0));
   switch (op) {
     case kPageCopy: return launch_pdl(plan_kernel<kPageCopy>, grid, kPlan, 0, s, p);

@@ -14,7 +14,7 @@ struct PagePlan {
   int* n_moves;
   int2* moves;     // (source page, destination page), [num_blocks]; a negative source is left out
   int* free_list;  // [num_blocks]
-  int* place;      // [num_blocks]: a page's new place (compact), marks (copy)
+  int* place;      // [num_blocks]: a page's new place (compact), marks (copy), counts before the call (resize)
   int* first;      // [max_rows]: first child of a row (fork)
   int* entries;    // [max_rows]: entries of a new row (fork); -1: the row failed (resize)
   int* fresh;      // [max_rows]: a row's own last page or -1 (fork); where its pages start in free_list (resize)

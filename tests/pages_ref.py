@@ -67,21 +67,21 @@ def resize(table, lengths, delta, ref, bs, MB):
             out.append(was)
             continue
         row = table[r]
-        want = [c for c in range(-(-was // bs), -(-now // bs)) if row[c] < 0]
-        shared = now > was and was % bs and row[was // bs] >= 0 and before[row[was // bs]] > 1
-        need = len(want) + bool(shared)
+        # entries that hold a position of [was, now): those of a page that other rows hold too become fresh pages, and
+        # so do those without one, unless a position below `was` lies there as well
+        want = [c for c in range(was // bs, -(-now // bs)) if now > was and
+                (before[row[c]] > 1 if row[c] >= 0 else c * bs >= was)]
+        need = len(want)
         first, at = at, at + need
         if need and at > len(free):
             failed.append(r)
             out.append(was)
             continue
-        if shared:
-            moves.append((row[was // bs], free[first]))
-            ref[row[was // bs]] -= 1
-            row[was // bs] = free[first]
-            ref[free[first]] = 1
-            first += 1
         for k, c in enumerate(want):
+            if row[c] >= 0:
+                if c * bs < was:  # positions below `was` lie there: its bytes go along
+                    moves.append((row[c], free[first + k]))
+                ref[row[c]] -= 1
             row[c] = free[first + k]
             ref[free[first + k]] = 1
         for c in range(-(-now // bs), MB):
