@@ -608,8 +608,8 @@ PA_API const char* pa_tree_last_error_message(pa_tree_handle h);
  * A sequence's new rows go to slots past[b] + j through block_table, as in
  * pa_cache_write (-1 writes nothing).  Rows at and behind cum[batch]
  * (cum[batch] <= token_count) are padding: neither read into the pools nor
- * written.  A sequence with a bad length is flagged and left out, its rows
- * as they were. */
+ * written.  A sequence with a bad length (one that ends behind token_count
+ * too) is flagged and left out, its rows as they were. */
 
 /* PB for a block_size (a power of two >= 16) and head_size (64, 128, 256); 0 for others. */
 PA_API int64_t pa_q4_page_bytes(int block_size, int head_size);

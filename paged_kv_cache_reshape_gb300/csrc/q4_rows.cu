@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) q4_rows_kernel(
         else hi = mid - 1;
       }
       const int c0 = g.cum[lo], c1 = g.cum[lo + 1], past = g.past[lo];
-      if (t < c0 || t >= c1 || c0 < 0) {
+      if (t < c0 || t >= c1 || c0 < 0 || c1 > g.T) {
         if (note) atomicOr(g.err, PA_DEVERR_CUM);
       } else if (past < 0) {
         if (note) atomicOr(g.err, PA_DEVERR_PAST);
