@@ -594,7 +594,7 @@ PA_API const char* pa_tree_last_error_message(pa_tree_handle h);
 
 /* ---- pools held in 4 bits ----
  *
- * A cache of a quarter of the bytes.  key_cache and value_cache are uint8
+ * A cache of 9/32 of the bytes of fp16.  key_cache and value_cache are uint8
  * [NB, Hk, PB], PB = bs * (D/2 + D/16): a page's share of one kv head is one
  * run, the codes of its bs rows (D/2 bytes each), then fp16 scales
  * [D/32, bs].  32 consecutive channels of a row share a scale.  Channel c of
@@ -661,11 +661,14 @@ PA_API pa_status pa_q4_read(pa_q4_handle h, const void* key_cache, const void* v
  * slot of a NaN scale makes the row NaN (its K) or those channels (its V).
  * query and output [T, H*D] dense; output must not overlap the inputs.
  * Scores, sums and the output accumulate in fp32.  A weight times V's scale is
- * rounded to fp16 once; of a sequence with more than 32 rows (new tokens x
- * H / Hk; 48 in a call with at most 28 batch rows, its token_count x H / Hk)
- * at head_size 64 or 128 the weights and the values of K and V are rounded to
- * fp16, once each, and a slot of V with a NaN scale makes the whole row
- * NaN. */
+ * rounded to fp16 once.  Sequences of many rows (new tokens x H / Hk) are
+ * computed in another way at head_size 64 and 128: an eighth of each value of K
+ * and V is rounded to fp16 (values below 2^-11 thus to multiples of 2^-21) and
+ * so are the weights, once where they are at least 2^-19 of the largest, and a
+ * slot of V with a NaN scale makes the whole row NaN.  Those are sequences of
+ * more than 32 rows, 48 in a call with at most 28 batch rows (its token_count x
+ * H / Hk), in calls with more tokens than batch or H / Hk > 8; in other calls
+ * (single tokens, as a rule) no sequence is, however long. */
 PA_API pa_status pa_q4_attention(pa_q4_handle h, const void* query, const void* key_cache, const void* value_cache,
                                  const int32_t* block_table, const int32_t* cumulative_sequence_lengths,
                                  const int32_t* past_sequence_lengths, int batch, int token_count,

@@ -999,7 +999,10 @@ cudaError_t launch_q4_attention(const Q4Params& p0, cudaStream_t s) {
   // 8 rows a unit where a sequence's rows are that few (one token each of up
   // to 8 heads a kv head), else 16: the codes of a key are made into operands
   // once for all rows of a unit.  head_size 256 has registers for 8.
-  const bool single = p.g.T <= p.g.batch && p.G <= 8;  // (as a rule)
+  // (As a rule: with T <= batch most sequences have a token each.  A chunk among
+  // empty slots is right too, but reads its keys once for 8 rows; the host cannot
+  // tell, and a launch that serves no sequence would cost each such call 6 us.)
+  const bool single = p.g.T <= p.g.batch && p.G <= 8;
   const int nt = p.g.D < 256 && !single ? 2 : 1;
   // Sequences of more rows than two such units go to the tcgen05 kernel, whose
   // time hardly depends on their number up to a tile's 128 (32 sequences of

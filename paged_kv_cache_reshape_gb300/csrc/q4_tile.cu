@@ -35,10 +35,11 @@
 // the instruction caches hold (fetch at 66 % of its peak), hence the loops
 // below that could be unrolled.
 //
-// Roundings beyond the scores' and sums' 32 bits: a K or V value to fp16 (its
-// code times its scale has up to 14 bits), a weight to fp16.  The outputs of
-// those chunks are 4.9e-4 off (relative, root mean square), 2.1e-4 of it their
-// own rounding to fp16.
+// Roundings beyond the scores' and sums' 32 bits: an eighth of a K or V value to
+// fp16 (a code times its scale has up to 14 bits; values below 2^-11 go to
+// multiples of 2^-21), a weight to fp16.  The outputs of those chunks are
+// 4.9e-4 off (relative, root mean square), 2.1e-4 of it their own rounding to
+// fp16.
 //
 // Roles (640 threads, one CTA per SM; registers moved between warpgroups):
 //   warpgroups 0, 1: tile A, B: the query's operand, softmax, output

@@ -5,7 +5,7 @@ import torch
 
 import paged_kv_cache_reshape_gb300 as pa
 import q4_ref
-from test_gpu_q4 import BF16, F16, expect_written, handle, rows_step, same_pool
+from test_gpu_q4 import BF16, F16, attend, check, expect_written, handle, rows_step, same_pool
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,38 @@ def test_a_long_tail_below_one_strong_key(n, strong):
     tol = tail * (2.0 ** -11 * 2 + off) + 7 * keys * 2.0 ** -30 + 136 * 2.0 ** -24
     assert ((got[..., 32:] - tail).abs() <= tol).all(), float((got[..., 32:] - tail).abs().max())
     assert ((got[..., :32] - top).abs() <= top * (2.0 ** -11 * 2 + off) + 136 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [40, 150])
+def test_small_keys_and_values_under_many_rows(D, n):
+    """K and V around 1e-3, where the operands (eighths of the values) are off by half of fp16's smallest number: a value
+    by 2^-22, so a score by that times the query's magnitudes (the bound of q4_ref has V's part)."""
+    scale = 0.1
+    c = q4_ref.make_case([300, 20], [n, 5], 4, 2, D, 16, q_std=150.0, scale=scale, v_std=1e-3, seed=D + n)
+    held = c["key_cache"][:, :, 16 * D // 2:].view(F16)
+    held *= 2.0 ** -10
+    op, out = attend(c)
+    assert op.device_error() == 0
+    ref, tol = q4_ref.attention(c)
+    got = out.double().cpu().view(c["T"], 4, D)
+    off = scale * 2.0 ** -22 * c["query"].double().abs().view(c["T"], 4, D).sum(2, keepdim=True)
+    assert ((got - ref).abs() <= tol + 2.2 * off * 6e-3).all()  # (in the weights: of V, below 6e-3)
+    assert (got - ref).norm() <= 2.0 ** -8 * ref.norm()
+
+
+def test_a_chunk_among_empty_slots():
+    """No more tokens than batch rows, all but one of them of one sequence: computed as single tokens are, so that a NaN
+    scale of V reaches its channels only."""
+    c = q4_ref.make_case([500] + [7] * 80, [75] + [0] * 79 + [1], 16, 2, 128, 16, seed=9)
+    clean, tol = q4_ref.attention(c)
+    op, out = attend(c)
+    check(c, out)
+    p = 520
+    c["value_cache"][int(c["table"][0, p // 16])][:, 16 * 64:].view(F16)[:, 16 + p % 16] = float("nan")
+    got = attend(c, op)[1].double().cpu().view(c["T"], 16, 128)
+    hit = torch.zeros(c["T"], 16, 128, dtype=torch.bool)
+    hit[20:75, :, 32:64] = True
+    assert got[hit].isnan().all() and not got[~hit].isnan().any()
+    assert ((got - clean).abs() <= tol)[~hit].all()
+    assert op.device_error() == 0
