@@ -466,6 +466,21 @@ def _gaps():
                                        "pa_tree_write)")
 
 
+_types = None  # torch's int32, float16 and bfloat16, once a call has tensors
+
+
+def _torch_types():
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.int32, torch.float16, torch.bfloat16)
+    return _types
+
+
+def _not_int32():
+    raise PAError(PA_INVALID_ARGUMENT, "tables, lengths, ids and counts must be int32")
+
+
 def _optional(t):
     if t is None:
         return None
@@ -636,12 +651,38 @@ def pa_q4_destroy(h):
     _q4_check(lib().pa_q4_destroy(h), None)
 
 
-def pa_q4_write(h, key, value, key_cache, value_cache, block_table, cumulative_sequence_lengths,
-                past_sequence_lengths, batch, token_count, stream=None):
-    """Rows of key and value [T, kv_num_heads * head_size] (their own row strides) into the pools."""
+def _q4_args(rows, other_rows, token_count, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+             past_sequence_lengths, batch, sizes):
+    """What the C calls cannot see: gaps, types and sizes (sizes: of a PagedQ4's configuration)."""
+    i32 = (_types or _torch_types())[0]
     if not (key_cache.is_contiguous() and value_cache.is_contiguous() and block_table.is_contiguous()
             and cumulative_sequence_lengths.is_contiguous() and past_sequence_lengths.is_contiguous()):
         _gaps()
+    if not (block_table.dtype is i32 and cumulative_sequence_lengths.dtype is i32
+            and past_sequence_lengths.dtype is i32):
+        _not_int32()
+    if cumulative_sequence_lengths.numel() <= batch or past_sequence_lengths.numel() < batch:
+        raise PAError(PA_INVALID_ARGUMENT, f"cumulative_sequence_lengths must have batch + 1 = {batch + 1} entries, "
+                                           f"past_sequence_lengths {batch}")
+    if sizes:
+        columns, pool_bytes, kind, width = sizes
+        if key_cache.nbytes != pool_bytes or value_cache.nbytes != pool_bytes:
+            raise PAError(PA_INVALID_ARGUMENT, f"pools must have {pool_bytes} bytes")
+        shape = block_table.shape
+        if len(shape) != 2 or shape[1] != columns or shape[0] < batch:
+            raise PAError(PA_INVALID_ARGUMENT, f"block_table must have {columns} columns and a row for each of the "
+                                               f"{batch} sequences")
+        if not (rows.dtype is kind and other_rows.dtype is kind):
+            raise PAError(PA_INVALID_ARGUMENT, f"rows must be {kind}")
+        if rows.numel() < token_count * width or other_rows.numel() < token_count * width:
+            raise PAError(PA_INVALID_ARGUMENT, f"{token_count} rows of {width} values are needed")
+
+
+def pa_q4_write(h, key, value, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+                past_sequence_lengths, batch, token_count, stream=None, sizes=None):
+    """Rows of key and value [T, kv_num_heads * head_size] (their own row strides) into the pools."""
+    _q4_args(key, value, token_count, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+             past_sequence_lengths, batch, sizes)
     st = (_lib or lib()).pa_q4_write(
         h, key.data_ptr(), _row_stride(key, token_count), value.data_ptr(), _row_stride(value, token_count),
         key_cache.data_ptr(), value_cache.data_ptr(), block_table.data_ptr(), cumulative_sequence_lengths.data_ptr(),
@@ -651,11 +692,10 @@ def pa_q4_write(h, key, value, key_cache, value_cache, block_table, cumulative_s
 
 
 def pa_q4_read(h, key_cache, value_cache, block_table, cumulative_sequence_lengths, past_sequence_lengths, batch,
-               token_count, key_out, value_out, stream=None):
+               token_count, key_out, value_out, stream=None, sizes=None):
     """The values held in slots past + j, to rows of key_out and value_out (their own row strides)."""
-    if not (key_cache.is_contiguous() and value_cache.is_contiguous() and block_table.is_contiguous()
-            and cumulative_sequence_lengths.is_contiguous() and past_sequence_lengths.is_contiguous()):
-        _gaps()
+    _q4_args(key_out, value_out, token_count, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+             past_sequence_lengths, batch, sizes)
     st = (_lib or lib()).pa_q4_read(
         h, key_cache.data_ptr(), value_cache.data_ptr(), block_table.data_ptr(),
         cumulative_sequence_lengths.data_ptr(), past_sequence_lengths.data_ptr(), batch, token_count,
@@ -666,11 +706,11 @@ def pa_q4_read(h, key_cache, value_cache, block_table, cumulative_sequence_lengt
 
 
 def pa_q4_attention(h, query, key_cache, value_cache, block_table, cumulative_sequence_lengths,
-                    past_sequence_lengths, batch, token_count, output, head_sink=None, stream=None):
-    if not (query.is_contiguous() and output.is_contiguous() and key_cache.is_contiguous()
-            and value_cache.is_contiguous() and block_table.is_contiguous()
-            and cumulative_sequence_lengths.is_contiguous() and past_sequence_lengths.is_contiguous()):
+                    past_sequence_lengths, batch, token_count, output, head_sink=None, stream=None, sizes=None):
+    if not (query.is_contiguous() and output.is_contiguous()):
         _gaps()
+    _q4_args(query, output, token_count, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+             past_sequence_lengths, batch, sizes)
     st = (_lib or lib()).pa_q4_attention(
         h, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_table.data_ptr(),
         cumulative_sequence_lengths.data_ptr(), past_sequence_lengths.data_ptr(), batch, token_count,
@@ -694,18 +734,31 @@ class PagedQ4:
         self.handle = None
         self.cfg, self.first_tokens = cfg, first_tokens
         self.handle = pa_q4_create(cfg, first_tokens)
+        kind = _torch_types()[2 if cfg.cache_dtype == PA_CACHE_BF16 else 1]
+        pool_bytes = cfg.num_blocks * cfg.kv_num_heads * pa_q4_page_bytes(cfg.block_size, cfg.head_size)
+        self.row_sizes = (cfg.max_blocks_per_seq, pool_bytes, kind, cfg.kv_num_heads * cfg.head_size)
+        self.query_sizes = (*self.row_sizes[:3], cfg.num_heads * cfg.head_size)
 
     def pool(self, device="cuda"):
         return q4_pool(self.cfg, device)
 
-    def write(self, *args, **kw):
-        pa_q4_write(self.handle, *args, **kw)
+    def write(self, key, value, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+              past_sequence_lengths, batch, token_count, stream=None):
+        pa_q4_write(self.handle, key, value, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+                    past_sequence_lengths, batch, token_count, stream, self.row_sizes)
 
-    def read(self, *args, **kw):
-        pa_q4_read(self.handle, *args, **kw)
+    def read(self, key_cache, value_cache, block_table, cumulative_sequence_lengths, past_sequence_lengths, batch,
+             token_count, key_out, value_out, stream=None):
+        pa_q4_read(self.handle, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+                   past_sequence_lengths, batch, token_count, key_out, value_out, stream, self.row_sizes)
 
-    def attention(self, *args, **kw):
-        pa_q4_attention(self.handle, *args, **kw)
+    def attention(self, query, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+                  past_sequence_lengths, batch, token_count, output, head_sink=None, stream=None):
+        if head_sink is not None and (head_sink.dtype is not self.query_sizes[2]
+                                      or head_sink.numel() < self.cfg.num_heads):
+            raise PAError(PA_INVALID_ARGUMENT, f"head_sink must be {self.query_sizes[2]}, a value for each head")
+        pa_q4_attention(self.handle, query, key_cache, value_cache, block_table, cumulative_sequence_lengths,
+                        past_sequence_lengths, batch, token_count, output, head_sink, stream, self.query_sizes)
 
     def device_error(self) -> int:
         return pa_q4_check_device_error(self.handle)
@@ -758,6 +811,9 @@ def pa_pages_copy(h, pools, src, dst, stream=None):
     """Page dst[i] of every pool receives page src[i]; pools: a page_pools."""
     if not (src.is_contiguous() and dst.is_contiguous()):
         _gaps()
+    i32 = (_types or _torch_types())[0]
+    if not (src.dtype is i32 and dst.dtype is i32):
+        _not_int32()
     if src.numel() != dst.numel():
         raise PAError(PA_INVALID_ARGUMENT, "src and dst must have the same length")
     st = (_lib or lib()).pa_pages_copy(h, pools.pointers, pools.num_pools, src.data_ptr(), dst.data_ptr(),
@@ -773,6 +829,10 @@ def pa_pages_fork(h, pools, block_table, lengths, parent, ref_count, new_block_t
             and ref_count.is_contiguous() and new_block_table.is_contiguous() and new_lengths.is_contiguous()
             and new_ref_count.is_contiguous()):
         _gaps()
+    i32 = (_types or _torch_types())[0]
+    if not (block_table.dtype is i32 and lengths.dtype is i32 and parent.dtype is i32 and ref_count.dtype is i32
+            and new_block_table.dtype is i32 and new_lengths.dtype is i32 and new_ref_count.dtype is i32):
+        _not_int32()
     rows, new_rows = block_table.shape[0], new_block_table.shape[0]
     if lengths.numel() != rows or parent.numel() != new_rows or new_lengths.numel() != new_rows:
         raise PAError(PA_INVALID_ARGUMENT, "lengths must have block_table's rows, parent and new_lengths "
@@ -790,6 +850,10 @@ def pa_pages_resize(h, pools, block_table, lengths, delta, new_lengths, ref_coun
     if not (block_table.is_contiguous() and lengths.is_contiguous() and delta.is_contiguous()
             and new_lengths.is_contiguous() and ref_count.is_contiguous()):
         _gaps()
+    i32 = (_types or _torch_types())[0]
+    if not (block_table.dtype is i32 and lengths.dtype is i32 and delta.dtype is i32 and new_lengths.dtype is i32
+            and ref_count.dtype is i32):
+        _not_int32()
     rows = block_table.shape[0]
     if lengths.numel() != rows or delta.numel() != rows or new_lengths.numel() != rows:
         raise PAError(PA_INVALID_ARGUMENT, "lengths, delta and new_lengths must have block_table's rows")
@@ -805,6 +869,10 @@ def pa_pages_compact(h, pools, block_table, ref_count, new_block_table, new_ref_
     if not (block_table.is_contiguous() and ref_count.is_contiguous() and new_block_table.is_contiguous()
             and new_ref_count.is_contiguous() and pages_in_use.is_contiguous()):
         _gaps()
+    i32 = (_types or _torch_types())[0]
+    if not (block_table.dtype is i32 and ref_count.dtype is i32 and new_block_table.dtype is i32
+            and new_ref_count.dtype is i32 and pages_in_use.dtype is i32):
+        _not_int32()
     if block_table.shape != new_block_table.shape:
         raise PAError(PA_INVALID_ARGUMENT, "block_table and new_block_table must have the same shape")
     st = (_lib or lib()).pa_pages_compact(

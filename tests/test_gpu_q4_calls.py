@@ -106,3 +106,27 @@ def test_a_chunk_among_empty_slots():
     assert got[hit].isnan().all() and not got[~hit].isnan().any()
     assert ((got - clean).abs() <= tol)[~hit].all()
     assert op.device_error() == 0
+
+
+def test_a_handle_refuses_other_types_and_sizes():
+    c = q4_ref.make_case([30, 20], [2, 1], 4, 2, 64, 16, sink=True)
+    op, good = handle(c), [c[k].cuda() for k in ("query", "key_cache", "value_cache", "table", "cum", "past_t")]
+    out, key = torch.zeros_like(good[0]), torch.zeros(c["T"], 128, dtype=F16, device="cuda")
+    op.attention(*good, 2, c["T"], out, head_sink=c["sink"].cuda())
+    op.write(key, key, *good[1:], 2, c["T"])
+    bad = [good[0].float(), good[1][:-1], good[2].half(), good[3][:, 1:].contiguous(), good[4].long(), good[5].long()]
+    for k, x in enumerate(bad):
+        args = good[:k] + [x] + good[k + 1:]
+        with pytest.raises(pa.PAError):
+            op.attention(*args, 2, c["T"], out)
+        if k:
+            with pytest.raises(pa.PAError):
+                op.write(key, key, *args[1:], 2, c["T"])
+            with pytest.raises(pa.PAError):
+                op.read(*args[1:], 2, c["T"], key, out)
+    with pytest.raises(pa.PAError):
+        op.write(key[:, :64], key, *good[1:], 2, c["T"])
+    for sink in (c["sink"].cuda().float(), c["sink"][:3].cuda()):
+        with pytest.raises(pa.PAError):
+            op.attention(*good, 2, c["T"], out, head_sink=sink)
+    assert op.device_error() == 0
