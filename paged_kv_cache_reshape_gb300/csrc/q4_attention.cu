@@ -53,6 +53,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kUnit = 5.9604644775390625e-8f;  // 2^-24, what a code of 1 stands for
 constexpr float kSlack = 4.f;
+constexpr int kNoTiles = 0x7fffffff;  // stream_rows of a call without the tcgen05 kernel
 constexpr int kSegSteps = 128;   // most steps of a segment
 constexpr int kSegRing = 4;
 constexpr int kMaxWarps = 20;
@@ -508,7 +509,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas) q4_st
     fence_mbar_init();
   }
   griddep_wait();
-  griddep_launch_dependents();
+  // The next kernel's CTAs may come as soon as there is room.  Not before the
+  // end where it is the tcgen05 kernel at head_size 64: that one leaves 90 KB
+  // of an SM to its L1, but only if it starts on an empty one; among this
+  // kernel's CTAs it keeps their 28 KB (32 x 260 rows after 3,000 tokens 251 us
+  // instead of 229, up to 800 rows a sequence 281 instead of 249).  At 128 it
+  // needs all shared memory itself, and the end is worth -2 % to +2 %.
+  if (D != 64 || p.stream_rows == kNoTiles) griddep_launch_dependents();
 
   // The line: every thread sums a share of the sequences, and the one whose
   // share holds the start of this CTA's range finds the sequence.
@@ -1015,7 +1022,7 @@ cudaError_t launch_q4_attention(const Q4Params& p0, cudaStream_t s) {
   const long long rows = (long long)p.g.T * p.G;
   const int stream_rows = rows <= 28LL * p.g.batch ? 48 : 32;
   const bool tiles = nt == 2 && rows > stream_rows;
-  p.stream_rows = tiles ? stream_rows : 0x7fffffff;
+  p.stream_rows = tiles ? stream_rows : kNoTiles;
   return dispatch(p, nt, tiles, false, s);
 }
 
