@@ -640,14 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 
       float m_ref = -INFINITY, l = 0.f;
       const int i_first = share ? X : 0, i_step = share ? 2 : 1;
-      // The unit's first scores before its masks: a wait for masks alone
-      // cannot tell a turn of their ring from the one two turns later, and B,
-      // which skips units without a tile B, may be that far ahead of the
-      // warps that write them.  With a tile's scores there, its K and every V
-      // up to two tiles before it have been made, so this tile's masks and
-      // the next ones' are at most a turn away.  (Scores before masks in each
-      // tile: the chunks above take 631 us.)
-      bool ok = warp_wait(&ctl->s_full[X], scnt & 1, abort, p.g.err, p.err_site, kSite | 7);
+      // B waits for the unit's first scores before its masks: a wait for masks
+      // alone cannot tell a turn of their ring from the one two turns later,
+      // and B, which skips units without a tile B, may be that far ahead of
+      // the warps that write them.  With a tile's scores there, its K and every
+      // V up to two tiles before it have been made, so this tile's masks and
+      // the next ones' are at most a turn away.  A has had every unit's output
+      // by then, which says as much.  (Scores before masks in each tile: the
+      // chunks above take 631 us.)
+      bool ok = X == 0 || warp_wait(&ctl->s_full[X], scnt & 1, abort, p.g.err, p.err_site, kSite | 7);
       if (!ok) break;
       for (int i = i_first; i < n; i += i_step) {
         const uint32_t tile = g + i;
