@@ -654,7 +654,8 @@ PA_API pa_status pa_q4_read(pa_q4_handle h, const void* key_cache, const void* v
 /* Causal attention of every packed query row over its sequence's pages (the
  * new rows already written).  Row (t, h) at position pos = past[b] + j admits
  * the mapped positions p <= pos; with local_window_size W those with
- * p > pos - W or p < first_tokens.  x = scale <q, k>, softcapped; output =
+ * p > pos - W or p < first_tokens.  x = scale <q, k>, softcapped (off by at
+ * most 2^-20 of the cap); output =
  * sum softmax(x) v, 0 when nothing is admitted; head_sink [H] (activations'
  * type, may be NULL) adds exp(sink_h) to the denominator.  A key that a row
  * does not admit never reaches that row, whatever its slot holds; an admitted

@@ -128,8 +128,10 @@ struct Cfg {
 
 // What a sequence adds to the line: row blocks x kv heads x the span of a
 // unit, its steps and about as many more as its start, joining and output
-// take the time of (a batch of 64 x 8 units of 500 to 4100 tokens takes 63 us
-// with 36, 67 with 24, 78 without).
+// take the time of.  64 x 8 units of 500 to 4,100 tokens, heads of 128: 63 us
+// with 36, 69 with 18, 66 with 72, 78 without; 200 x 8 of 200 to 2,500: 122,
+// 132 and 124 us, heads of 64: 74, 81 and 78.  head_size 256, 200 x 4 of them:
+// 105 us with 24, 114 with 12, 107 with 36; the window's 40 x 4: 64 with each.
 template <int D>
 constexpr int kUnitSpan = D == 256 ? 24 : 36;
 struct SeqWork {
@@ -543,7 +545,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas) q4_st
   // (None but those behind the last is empty, and none shorter than kLeast:
   // the warps take that many steps at once anyway, and a unit in fewer pieces
   // is joined sooner.  One user over 600 tokens: 19 us with ranges of 4, 15.5
-  // with 32, 17.8 with 96.)
+  // with 32, 17.8 with 96; over 4,000: 16.8 with 32, 19.2 with 16, 20.2 with
+  // 64, head_size 256 23.1, 23.9 and 24.7.)
   constexpr int kLeast = 32;
   const long long ranges = min((long long)gridDim.x, (total + kLeast - 1) / kLeast), me = min((long long)blockIdx.x, ranges);
   const long long r0 = ranges ? total * me / ranges : 0, r1 = me < ranges ? total * (me + 1) / ranges : r0;
@@ -1014,11 +1017,13 @@ cudaError_t launch_q4_attention(const Q4Params& p0, cudaStream_t s) {
   // Sequences of more rows than two such units go to the tcgen05 kernel, whose
   // time hardly depends on their number up to a tile's 128 (32 sequences of
   // 3000 tokens, 8 kv heads of 128: 32 rows take 126 us here and 136 there, 36
-  // rows 157 and 135).  Where most have fewer, a sequence of up to three units
+  // rows 167 and 133).  Where most have fewer, a sequence of up to three units
   // is better left here, for the few that there are (1 to 9 tokens of 4 heads
-  // after up to 3000: 79 us with three, 94 with two; rows of 36 in every
-  // sequence would take 165 and 135).  The mean decides, as the host knows no
-  // sequence's rows.
+  // after up to 3000: 79 us with three, 95 with two; heads of 64 48 and 59; 64
+  // sequences of 1 to 6 tokens of 8 heads 78 and 101; rows of 36 in every
+  // sequence would take 166 and 133, heads of 64 94 and 82).  The mean decides,
+  // as the host knows no sequence's rows: above 28 calls of 1 to 12 tokens of
+  // 4 heads (mean 28.5) lose 90 -> 103, but ones of equal rows gain as much.
   const long long rows = (long long)p.g.T * p.G;
   const int stream_rows = rows <= 28LL * p.g.batch ? 48 : 32;
   const bool tiles = nt == 2 && rows > stream_rows;
