@@ -358,10 +358,12 @@ __device__ __forceinline__ void take_steps(const Q4Params& p, Share<D, NT>& w, c
         // the old reference is that of a score lim - kSlack (none yet: lim = -inf)
         top = fmaxf(top, w.lim[nt][e] - kSlack);
         const bool none = top == -INFINITY;
-        const float r1 = none ? 0.f : top - k;
+        // (rounded up and the limit down: for scores past 2^24 a rounding may
+        // be more than a weight's exponent has left)
+        const float r1 = none ? 0.f : __fadd_ru(top, -k);
         up[nt][e] = w.lim[nt][e] == -INFINITY ? 0.f : ex2(w.ref[nt][e] - r1);
         w.ref[nt][e] = r1;
-        w.lim[nt][e] = none ? -INFINITY : top + kSlack;
+        w.lim[nt][e] = none ? -INFINITY : __fadd_rd(top, kSlack);
         w.l[nt][e] *= up[nt][e];
       }
 #pragma unroll
@@ -487,7 +489,10 @@ __device__ __forceinline__ void lay_out_query(const Q4Params& p, int t0, int h, 
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (t == 0) to.c0[nt][j][g] = s * (-8.f * kUnit);
     }
-    if (t == 0) to.f[nt][g] = ldexpf(CAP ? 2.f * kLog2e * p.scale / p.softcap : p.scale * kLog2e, 24 - up);
+    // (finite where the scores are: the largest queries' exponent and the codes'
+    // 2^24 together may pass 2^127, and scores of 0 have to stay 0)
+    const float f = ldexpf(CAP ? 2.f * kLog2e * p.scale / p.softcap : p.scale * kLog2e, 24 - up);
+    if (t == 0) to.f[nt][g] = fminf(f, 3.402823466e38f);
   }
 }
 

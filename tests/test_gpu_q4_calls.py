@@ -130,3 +130,17 @@ def test_a_handle_refuses_other_types_and_sizes():
         with pytest.raises(pa.PAError):
             op.attention(*good, 2, c["T"], out, head_sink=sink)
     assert op.device_error() == 0
+
+
+@pytest.mark.parametrize("n", [1, 9])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("q_std", [1e8, 3e9, 1e12, 1e30, 4e37])
+def test_very_large_queries(q_std, softcap, n):
+    """Scores that are finite in 32 bits, up to their largest.  One key takes all, or with a cap those of positive
+    scores; keys of score 0 are no NaN.  K's scales are a power of two, so that its values lose no bits anywhere and
+    which key is the largest is as good as certain."""
+    c = q4_ref.make_case([200, 60], [n, 1], 4, 2, 128, 16, q_std=q_std, scale=0.01, softcap=softcap, dtype=BF16, seed=n)
+    held = c["key_cache"][:, :, 16 * 64:].view(F16)
+    held[~held.isnan()] = 0.5
+    held[c["table"][0, 0].item()] = 0.0  # 16 keys whose scores are 0
+    check(c)
