@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->q_full[X]);
 
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = -INFINITY, l = 0.f, back = 1.f;  // (back: what the row's scores were divided by)
       const int i_first = share ? X : 0, i_step = share ? 2 : 1;
       // B waits for the unit's first scores before its masks: a wait for masks
       // alone cannot tell a turn of their ring from the one two turns later,
@@ -699,15 +699,27 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
 #pragma unroll
             for (int c = 0; c < kKeys; ++c) spoilt |= ((no_v[c >> 5] >> (c & 31)) & 1) && x[c] != -INFINITY;
           }
-          const float mul = CAP ? 1.f : f;
-          const float cand = max_tree<kKeys>(x) * mul;
+          const float cand = max_tree<kKeys>(x) * (CAP ? 1.f : f);
           float up = 1.f;
-          if (cand > m_ref + (kLift + kSlack) || (m_ref == -INFINITY && cand != -INFINITY)) {
-            const float to = ceilf(cand) - kLift;
+          if (cand > __fadd_rd(m_ref, kLift + kSlack) || (m_ref == -INFINITY && cand != -INFINITY)) {
+            float to = ceilf(cand) - kLift;
             up = __int_as_float((127 + max(__float2int_rn(m_ref - to), -127)) << 23);  // 2^(m_ref - to), 0 below 2^-126
+            // Past 2^24 a rounded reference lies further from the unrounded
+            // products below than the weights' exponents reach: the row's
+            // scores are taken in larger units from here on, in which the
+            // largest is below 2^24 and keys that differ at all in fp32
+            // still hardly share a weight.
+            const int by = (int)(__float_as_uint(cand) << 1 >> 24) - (127 + 23);  // (above 104: no number)
+            if (!CAP && by > 0 && by <= 104) {
+              const float down = __int_as_float((127 - by) << 23);
+              f *= down;
+              back *= __int_as_float((127 + by) << 23);
+              to = ceilf(cand * down) - kLift;
+            }
             m_ref = to;
             alpha *= up;
           }
+          const float mul = CAP ? 1.f : f;
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
           __syncwarp();
           if (half == 1 && __any_sync(0xffffffffu, up != 1.f)) {
@@ -764,6 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_tile_kernel(const __grid_const
       }
       g += n;
       if (!ok) break;
+      if constexpr (!CAP) m_ref *= back;
       if (share && X == 1) {  // A joins
         ++ocnt[1];
         b_sums[r] = make_float2(m_ref, l);

@@ -132,7 +132,7 @@ def test_a_handle_refuses_other_types_and_sizes():
     assert op.device_error() == 0
 
 
-@pytest.mark.parametrize("n", [1, 9])
+@pytest.mark.parametrize("n", [1, 9, 40, 150])
 @pytest.mark.parametrize("softcap", [0.0, 30.0])
 @pytest.mark.parametrize("q_std", [1e8, 3e9, 1e12, 1e30, 4e37])
 def test_very_large_queries(q_std, softcap, n):

@@ -120,3 +120,15 @@ def test_captured_calls_with_many_tiles():
         torch.cuda.synchronize()
         check(c, out)
     assert op.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", [SHORT_AND_LONG, SHARED], ids=["short_and_long", "shared"])
+def test_very_large_scores_over_many_tiles(shape, D):
+    """Scores around 1e9, whose largest grows from tile to tile: the tiles' and ranges' references are in other units."""
+    c = many_tiles(shape, D, BF16, seed=7, q_std=1e10, scale=0.01)
+    held = c["key_cache"][:, :, 32 * D // 2:].view(F16)
+    held[~held.isnan()] = 0.5  # (K's values lose no bits: the largest key is as good as certain)
+    op, out = attend(c)
+    check(c, out)
+    assert op.device_error() == 0
