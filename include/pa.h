@@ -708,9 +708,9 @@ PA_API pa_status pa_pages_create(const pa_pages_config* cfg, pa_pages_handle* ou
 PA_API pa_status pa_pages_destroy(pa_pages_handle h);
 
 /* In every pool page dst[i] receives page src[i], i < count <= NB (int32,
- * device).  A -1 on either side leaves the pair out.  No page may be a
- * destination twice, or a destination and a source: such pairs are skipped
- * and flagged (PA_DEVERR_PAGES). */
+ * device).  A -1 on either side leaves the pair out.  Pairs that name one
+ * destination are all left out and flagged (PA_DEVERR_PAGES), and so is a pair
+ * whose source is any pair's destination. */
 PA_API pa_status pa_pages_copy(pa_pages_handle h, void* const* pools, int num_pools, const int32_t* src,
                                const int32_t* dst, int count, void* stream);
 

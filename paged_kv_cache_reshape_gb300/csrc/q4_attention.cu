@@ -35,11 +35,13 @@
 //
 // What bounds it.  Two sequences of 100,000 to 131,072 tokens, 64 query heads
 // over 8 of 128: 262 MB in 75 us, 52 % of the copy rate; 64 sequences of 512 to
-// 4,096, 32 over 8: 172 MB in 63 us, 40 %.  About 330 instructions a step (the
-// codes' masks, the scales, two MMA chains, the softmax) issue 47 to 55 % of
-// the time with 11 or 12 warps of 162 registers, and the steady state of long
-// ranges reads at 64 to 68 % of the copy rate; about 15 us of a call are start,
-// the units' ends and the join.  One user over 600 tokens: 15 us, the latency
+// 4,096, 32 over 8: 172 MB in 63 us, 40 %.  Neither memory nor the issue slots
+// are full: about 330 instructions a step (the codes' masks, the scales, two
+// MMA chains, the softmax) issue 47 to 55 % of the time with 11 or 12 warps of
+// 162 registers, three to a scheduler, which wait for fixed latencies and at a
+// unit's end for one another.  The steady state of long ranges reads at 64 to
+// 68 % of the copy rate; about 15 us of a call are start, the units' ends and
+// the join.  One user over 600 tokens: 15 us, the latency
 // of two launches and a chain of 32 steps a range.
 #include <algorithm>
 

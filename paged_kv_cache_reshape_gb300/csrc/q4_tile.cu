@@ -22,18 +22,18 @@
 // the one tile's rows, over every other key tile each, with sums and outputs
 // of their own that A joins at the end.  Otherwise scores, softmax and product
 // of one key tile after the other wait for each other: 32 sequences of 36 rows
-// after 3,000 tokens, 8 kv heads of 128, take 158 us without and 135 with it.
+// after 3,000 tokens, 8 kv heads of 128, take 158 us without and 134 with it.
 // Calls with more than 128 rows to a sequence get a kernel without this part:
 // it costs them 2 % to 8 % (the chunks below: 577 us became 586).
 //
 // What bounds it.  Two chunks of 1,024 tokens after 8,000 to 16,000, 32 query
-// heads over 8 of 128: 570 us, where the products alone are 259 us at the
+// heads over 8 of 128: 575 us, where the products alone are 252 us at the
 // bf16 rate that a library product reaches.  The tensor cores are busy 36 % of
-// the time, instructions issue 45 %: each tile's scores, softmax, P and
-// product follow one another, and two tiles' S and O fill tensor memory, so
-// there is no third to fill the gaps.  The roles' code together is about what
-// the instruction caches hold (fetch at 66 % of its peak), hence the loops
-// below that could be unrolled.
+// the time, instructions issue 44 %: each tile's scores, softmax, P and
+// product follow one another, and at head_size 128 two tiles' S and O fill
+// tensor memory, so there is no third to fill the gaps.  The roles' code
+// together is about what the instruction caches hold (fetch at 70 % of its
+// peak), hence the loops below that could be unrolled.
 //
 // Roundings beyond the scores' and sums' 32 bits: an eighth of a K or V value to
 // fp16 (a code times its scale has up to 14 bits; values below 2^-11 go to
@@ -74,7 +74,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // and one 2^-19 as large still keeps all of its bits (with a reference at
 // the largest score, 8,192 keys of 2^-25.4 each were lost, 2e-4 of a row); and
 // what a move multiplies by is a power of two, which rounds no weight a second
-// time unless it falls below fp16's smallest normal.  Chunks 578 -> 581 us.
+// time unless it falls below fp16's smallest normal.
 constexpr float kLift = 6.f, kSlack = 8.f;
 constexpr int kSite = kSiteQ4 | 64;
 
